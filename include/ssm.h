@@ -100,6 +100,7 @@ typedef enum { SSM_MAMBA1 = 1, SSM_MAMBA2 = 2 } ssm_mode;
 #define SSM_DEVERR_CU_SEQLENS 1   /* cu_seqlens not 0-based, decreasing, or not ending at seqlen */
 #define SSM_DEVERR_TIMEOUT 2      /* a bounded wait for tensor-core completion ran out; outputs incomplete */
 #define SSM_DEVERR_BOUNDS 3       /* bounds-checked build only: an index fell outside its tensor (see ssm_bounds_record) */
+#define SSM_DEVERR_PAGES 4        /* a page call skipped an entry: page out of range, not live, taken, or none free */
 
 /* ------------------------------------------------------------------ conv */
 typedef struct ssm_conv_args {
@@ -412,6 +413,176 @@ SSM_API ssm_status ssm_split_combine(const ssm_split_args *args, void *stream);
  * this call has no workspace for an error word. */
 SSM_API ssm_status ssm_split_fixup(const ssm_scan_args *args, const float *cum_delta, const float *h_in,
                                    void *stream);
+
+/* ------------------------------------------------------ gated delta rule */
+/* The recurrence beside the scan whose write is corrected by what the state
+ * already answers for the key: per head, with state h [P][N] (row p, the
+ * layout of h_final),
+ *
+ *     a_t = exp(g_t)
+ *     u_t = beta_t (v_t - a_t h_{t-1} k_t)           [P]
+ *     h_t = a_t h_{t-1} + u_t k_t^T
+ *     y_t = scale * h_t q_t                          [P]
+ *
+ * h_0 = h0 (zeros when absent), h_T returned in h_final.  Keys and queries
+ * come in groups shared by nheads / ngroups consecutive heads, as B and C do
+ * in ssm_scan_fwd.  The rule is meant for keys of at most unit length and
+ * beta in [0, 1]; other values are computed as the formula stands.  g <= 0 is
+ * the log decay; g below -100 (-infinity included) counts as -100, whose
+ * exp() is zero in fp32.  A NaN or infinity reaches the other tokens of its
+ * own 64-token block and everything after it, never another sequence.
+ *
+ * q, k, v, y share one dtype; g and beta are fp32 whatever the dtype, since a
+ * log decay summed over a sequence does not survive 8 bits.  bf16 with
+ * dstate <= 128, dstate and headdim multiples of 8 and 16-byte aligned rows
+ * runs in 64-token blocks on the tensor cores; everything else (dstate <= 256)
+ * runs the recurrence token by token in fp32. */
+typedef struct ssm_delta_args {
+    int32_t dtype;            /* ssm_dtype of q, k, v, y */
+    int32_t nseqs;            /* number of sequences when cu_seqlens != NULL */
+    int64_t batch;            /* 1 when cu_seqlens != NULL */
+    int64_t seqlen;           /* tokens per row, or total packed tokens */
+    int64_t nheads, headdim;  /* H, P */
+    int64_t ngroups, dstate;  /* G (nheads % ngroups == 0), N */
+    const void *q;  int64_t q_batch_stride, q_token_stride;         /* [b][T][G*N] */
+    const void *k;  int64_t k_batch_stride, k_token_stride;         /* [b][T][G*N] */
+    const void *v;  int64_t v_batch_stride, v_token_stride;         /* [b][T][H*P] */
+    const float *g; int64_t g_batch_stride, g_token_stride;         /* [b][T][H] */
+    const float *beta; int64_t beta_batch_stride, beta_token_stride;/* [b][T][H] */
+    void *y;        int64_t y_batch_stride, y_token_stride;         /* [b][T][H*P] */
+    const float *h0;          /* [nseq][H][P][N] or NULL */
+    float *h_final;           /* [nseq][H][P][N] or NULL */
+    const int32_t *cu_seqlens;/* [nseqs+1] device int32, or NULL */
+    float scale;
+    int32_t reserved0;
+} ssm_delta_args;
+
+/* Backward of ssm_delta_fwd: gradients of sum(dy * y) + sum(dh_final *
+ * h_final) for the call `fwd` describes (its y and h_final are ignored).
+ * Gradients are contiguous.  dq, dk [b][T][G*N] (summed over the heads of a
+ * group), dv [b][T][H*P], dg, dbeta [b][T][H] are in the activations' dtype,
+ * each rounded once; dh0 [nseq][H][P][N] is fp32 and may be NULL.  Sums run
+ * in a fixed order: the same call gives the same bits. */
+typedef struct ssm_delta_bwd_args {
+    ssm_delta_args fwd;
+    const void *dy; int64_t dy_batch_stride, dy_token_stride;       /* like y (dtype) */
+    const float *dh_final;    /* [nseq][H][P][N] or NULL */
+    void *dq, *dk, *dv, *dg, *dbeta;
+    float *dh0;
+} ssm_delta_bwd_args;
+
+/* One token per batch row on slot-indexed fp32 states, in place. */
+typedef struct ssm_delta_update_args {
+    int32_t dtype, reserved0;
+    float scale;
+    int32_t reserved1;
+    int64_t batch, nheads, headdim, ngroups, dstate;
+    float *state;             /* in-out [nslots][H][P][N], 16-byte aligned when dstate % 4 == 0 */
+    const void *q;  int64_t q_batch_stride;   /* [b][G*N] */
+    const void *k;  int64_t k_batch_stride;
+    const void *v;  int64_t v_batch_stride;   /* [b][H*P] */
+    const float *g; int64_t g_batch_stride;   /* [b][H] */
+    const float *beta; int64_t beta_batch_stride;
+    void *y;        int64_t y_batch_stride;   /* [b][H*P] */
+    const int32_t *state_batch_indices;  /* [batch]: slot of row r (NULL = r).  A negative slot, or one
+                                            past nslots, marks a padding row: its y is set to 0 and no
+                                            state is touched.  Rows must name distinct slots. */
+    int64_t nslots;
+} ssm_delta_update_args;
+
+/* `workspace`: device, 256-byte aligned, ssm_delta_workspace_size() bytes;
+ * its error word is read with ssm_workspace_error. */
+SSM_API size_t ssm_delta_workspace_size(const ssm_delta_args *args);
+SSM_API ssm_status ssm_delta_fwd(const ssm_delta_args *args, void *workspace, size_t ws_bytes, void *stream);
+SSM_API size_t ssm_delta_bwd_workspace_size(const ssm_delta_bwd_args *args);
+SSM_API ssm_status ssm_delta_bwd(const ssm_delta_bwd_args *args, void *workspace, size_t ws_bytes, void *stream);
+/* No workspace. */
+SSM_API ssm_status ssm_delta_update(const ssm_delta_update_args *args, void *stream);
+
+/* ------------------------------------------------------------ group norm */
+/* Group norm of channels-last rows with an activation: every token's channels
+ * are split into `groups` equal runs, each normalised by its own statistics
+ * (never across tokens, so a causal layer stays causal):
+ *
+ *     s   = x * silu(z)  (SSM_NORM_GATE_FIRST)  or  x
+ *     n   = (s - mean) / sqrt(var + eps)         subtract_mean = 1
+ *     n   = s / sqrt(mean(s^2) + eps)            subtract_mean = 0
+ *     t   = n * weight + bias
+ *     y   = t | silu(t) | t * silu(z)            SSM_NORM_PLAIN, _GATE_FIRST | _SILU | _GATE
+ *
+ * Statistics and arithmetic are fp32; y is rounded once.  channels / groups
+ * is at most 16384.  y may be x (same strides). */
+typedef enum { SSM_NORM_PLAIN = 0, SSM_NORM_SILU = 1, SSM_NORM_GATE = 2, SSM_NORM_GATE_FIRST = 3 } ssm_norm_mode;
+typedef struct ssm_norm_args {
+    int32_t dtype;            /* ssm_dtype of x, z, y */
+    int32_t mode;             /* ssm_norm_mode */
+    int32_t subtract_mean;    /* 0 or 1 */
+    float eps;                /* >= 0 */
+    int64_t batch, seqlen, channels, groups;   /* channels % groups == 0 */
+    const void *x;  int64_t x_batch_stride, x_token_stride;
+    const void *z;  int64_t z_batch_stride, z_token_stride;   /* the gate modes only, else NULL */
+    void *y;        int64_t y_batch_stride, y_token_stride;
+    const float *weight, *bias;   /* [channels] or NULL (1, 0) */
+} ssm_norm_args;
+
+/* Gradients of sum(dy * y).  dx, dz [b][T][channels] contiguous in dtype (dz
+ * required when z is given); dweight, dbias [channels] fp32 or NULL.  The
+ * sums over tokens run in a fixed order. */
+typedef struct ssm_norm_bwd_args {
+    ssm_norm_args fwd;        /* y ignored */
+    const void *dy; int64_t dy_batch_stride, dy_token_stride;
+    void *dx, *dz;
+    float *dweight, *dbias;
+} ssm_norm_bwd_args;
+
+SSM_API ssm_status ssm_group_norm_fwd(const ssm_norm_args *args, void *stream);
+SSM_API size_t ssm_group_norm_bwd_workspace_size(const ssm_norm_bwd_args *args);
+SSM_API ssm_status ssm_group_norm_bwd(const ssm_norm_bwd_args *args, void *workspace, size_t ws_bytes, void *stream);
+
+/* ----------------------------------------------------------- state pages */
+/* The slots of a recurrent-state cache as pages: page i is row i of every
+ * pool (a state pool [nslots][H][P][N] and a conv pool [nslots][conv_dim][K-1],
+ * say), the slots that ssm_state_update, ssm_delta_update and the
+ * intermediate states of ssm_scan_fwd address.  `refs` [nslots] counts the
+ * holders of each page on the device; 0 marks a free one.  All calls run
+ * without a host round trip, and equal inputs give equal pages: the lowest
+ * free page goes first.
+ *
+ *   copy     pool[dst[i]] = pool[src[i]], zeros for src[i] = -1.  An entry is
+ *            skipped when dst[i] < 0 or src[i] == dst[i].
+ *   fork     for every entry in order: pages[i] = the lowest free page, refs
+ *            = 1, its contents those of page src[i] (which has to be live) or
+ *            zeros for src[i] = -1.  pages[i] = -1 when no page is left.
+ *   free     refs[pages[i]] -= 1 for pages[i] >= 0.  Contents stay.
+ *   compact  with n live pages, the i-th live page at or behind n moves to
+ *            the i-th free page before n; refs follow, and table[j] (page
+ *            numbers, e.g. one per sequence) is rewritten to the new number.
+ *            Negative entries stay; entries that name no live page become -1.
+ *
+ * A skipped entry sets SSM_DEVERR_PAGES in the workspace error word: a page
+ * number outside the pool, a copy whose dst an earlier entry writes or another
+ * entry reads, a fork of a page that is not live or with no free page left, a
+ * free of a page that is not held.  The other entries are carried out. */
+#define SSM_MAX_POOLS 8
+typedef struct ssm_page_pool {
+    void *base;               /* [nslots][page_bytes] */
+    int64_t page_bytes;       /* > 0 */
+} ssm_page_pool;
+typedef struct ssm_pages_args {
+    int64_t nslots;           /* pages in every pool, at most 2^20 */
+    int64_t n;                /* entries of src / pages (copy, fork, free) or table (compact) */
+    int32_t npools, reserved0;
+    ssm_page_pool pools[SSM_MAX_POOLS];
+    int32_t *refs;            /* [nslots]; fork, free, compact */
+    const int32_t *src;       /* [n]; copy, fork */
+    int32_t *pages;           /* [n]: copy (dst, read), fork (written), free (read), compact (table, in-out) */
+} ssm_pages_args;
+
+SSM_API size_t ssm_pages_workspace_size(const ssm_pages_args *args);
+SSM_API ssm_status ssm_pages_copy(const ssm_pages_args *args, void *workspace, size_t ws_bytes, void *stream);
+SSM_API ssm_status ssm_pages_fork(const ssm_pages_args *args, void *workspace, size_t ws_bytes, void *stream);
+SSM_API ssm_status ssm_pages_free(const ssm_pages_args *args, void *workspace, size_t ws_bytes, void *stream);
+SSM_API ssm_status ssm_pages_compact(const ssm_pages_args *args, void *workspace, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

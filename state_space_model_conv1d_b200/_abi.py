@@ -17,7 +17,7 @@ SSM_ERR_WORKSPACE, SSM_ERR_CUDA, SSM_ERR_DEVICE = -4, -5, -6
 SSM_F32, SSM_BF16 = 0, 1
 ABI_VERSION = 3                # SSM_ABI_VERSION of the header this mirror follows
 SSM_MAMBA1, SSM_MAMBA2 = 1, 2
-SSM_DEVERR_NONE, SSM_DEVERR_CU_SEQLENS, SSM_DEVERR_TIMEOUT, SSM_DEVERR_BOUNDS = 0, 1, 2, 3
+SSM_DEVERR_NONE, SSM_DEVERR_CU_SEQLENS, SSM_DEVERR_TIMEOUT, SSM_DEVERR_BOUNDS, SSM_DEVERR_PAGES = 0, 1, 2, 3, 4
 
 _vp = C.c_void_p
 _i64 = C.c_int64
@@ -97,6 +97,82 @@ class SplitArgs(C.Structure):
 
 
 # Every symbol the header declares, with its ctypes signature.
+class DeltaArgs(C.Structure):
+    _fields_ = [
+        ("dtype", _i32), ("nseqs", _i32),
+        ("batch", _i64), ("seqlen", _i64), ("nheads", _i64), ("headdim", _i64), ("ngroups", _i64), ("dstate", _i64),
+        ("q", _vp), ("q_batch_stride", _i64), ("q_token_stride", _i64),
+        ("k", _vp), ("k_batch_stride", _i64), ("k_token_stride", _i64),
+        ("v", _vp), ("v_batch_stride", _i64), ("v_token_stride", _i64),
+        ("g", _vp), ("g_batch_stride", _i64), ("g_token_stride", _i64),
+        ("beta", _vp), ("beta_batch_stride", _i64), ("beta_token_stride", _i64),
+        ("y", _vp), ("y_batch_stride", _i64), ("y_token_stride", _i64),
+        ("h0", _vp), ("h_final", _vp), ("cu_seqlens", _vp),
+        ("scale", C.c_float), ("reserved0", _i32),
+    ]
+
+
+class DeltaBwdArgs(C.Structure):
+    _fields_ = [
+        ("fwd", DeltaArgs),
+        ("dy", _vp), ("dy_batch_stride", _i64), ("dy_token_stride", _i64),
+        ("dh_final", _vp),
+        ("dq", _vp), ("dk", _vp), ("dv", _vp), ("dg", _vp), ("dbeta", _vp), ("dh0", _vp),
+    ]
+
+
+class DeltaUpdateArgs(C.Structure):
+    _fields_ = [
+        ("dtype", _i32), ("reserved0", _i32), ("scale", C.c_float), ("reserved1", _i32),
+        ("batch", _i64), ("nheads", _i64), ("headdim", _i64), ("ngroups", _i64), ("dstate", _i64),
+        ("state", _vp),
+        ("q", _vp), ("q_batch_stride", _i64),
+        ("k", _vp), ("k_batch_stride", _i64),
+        ("v", _vp), ("v_batch_stride", _i64),
+        ("g", _vp), ("g_batch_stride", _i64),
+        ("beta", _vp), ("beta_batch_stride", _i64),
+        ("y", _vp), ("y_batch_stride", _i64),
+        ("state_batch_indices", _vp), ("nslots", _i64),
+    ]
+
+
+SSM_NORM_PLAIN, SSM_NORM_SILU, SSM_NORM_GATE, SSM_NORM_GATE_FIRST = 0, 1, 2, 3
+
+
+class NormArgs(C.Structure):
+    _fields_ = [
+        ("dtype", _i32), ("mode", _i32), ("subtract_mean", _i32), ("eps", C.c_float),
+        ("batch", _i64), ("seqlen", _i64), ("channels", _i64), ("groups", _i64),
+        ("x", _vp), ("x_batch_stride", _i64), ("x_token_stride", _i64),
+        ("z", _vp), ("z_batch_stride", _i64), ("z_token_stride", _i64),
+        ("y", _vp), ("y_batch_stride", _i64), ("y_token_stride", _i64),
+        ("weight", _vp), ("bias", _vp),
+    ]
+
+
+class NormBwdArgs(C.Structure):
+    _fields_ = [
+        ("fwd", NormArgs),
+        ("dy", _vp), ("dy_batch_stride", _i64), ("dy_token_stride", _i64),
+        ("dx", _vp), ("dz", _vp), ("dweight", _vp), ("dbias", _vp),
+    ]
+
+
+SSM_MAX_POOLS = 8
+
+
+class PagePool(C.Structure):
+    _fields_ = [("base", _vp), ("page_bytes", _i64)]
+
+
+class PagesArgs(C.Structure):
+    _fields_ = [
+        ("nslots", _i64), ("n", _i64), ("npools", _i32), ("reserved0", _i32),
+        ("pools", PagePool * SSM_MAX_POOLS),
+        ("refs", _vp), ("src", _vp), ("pages", _vp),
+    ]
+
+
 SIGNATURES = {
     "ssm_abi_version": ([], _i32),
     "ssm_status_string": ([_i32], C.c_char_p),
@@ -116,6 +192,19 @@ SIGNATURES = {
     "ssm_split_cum_delta": ([C.POINTER(ScanArgs), _vp, _vp, _vp], _i32),
     "ssm_split_combine": ([C.POINTER(SplitArgs), _vp], _i32),
     "ssm_split_fixup": ([C.POINTER(ScanArgs), _vp, _vp, _vp], _i32),
+    "ssm_delta_workspace_size": ([C.POINTER(DeltaArgs)], C.c_size_t),
+    "ssm_delta_fwd": ([C.POINTER(DeltaArgs), _vp, C.c_size_t, _vp], _i32),
+    "ssm_delta_bwd_workspace_size": ([C.POINTER(DeltaBwdArgs)], C.c_size_t),
+    "ssm_delta_bwd": ([C.POINTER(DeltaBwdArgs), _vp, C.c_size_t, _vp], _i32),
+    "ssm_delta_update": ([C.POINTER(DeltaUpdateArgs), _vp], _i32),
+    "ssm_group_norm_fwd": ([C.POINTER(NormArgs), _vp], _i32),
+    "ssm_group_norm_bwd_workspace_size": ([C.POINTER(NormBwdArgs)], C.c_size_t),
+    "ssm_group_norm_bwd": ([C.POINTER(NormBwdArgs), _vp, C.c_size_t, _vp], _i32),
+    "ssm_pages_workspace_size": ([C.POINTER(PagesArgs)], C.c_size_t),
+    "ssm_pages_copy": ([C.POINTER(PagesArgs), _vp, C.c_size_t, _vp], _i32),
+    "ssm_pages_fork": ([C.POINTER(PagesArgs), _vp, C.c_size_t, _vp], _i32),
+    "ssm_pages_free": ([C.POINTER(PagesArgs), _vp, C.c_size_t, _vp], _i32),
+    "ssm_pages_compact": ([C.POINTER(PagesArgs), _vp, C.c_size_t, _vp], _i32),
     "ssm_check_bounds_enabled": ([], _i32),
     "ssm_bounds_record": ([C.POINTER(_i32), C.POINTER(_i32), C.POINTER(_i64), C.POINTER(_i64), _i32], _i32),
 }

@@ -1,0 +1,27 @@
+// delta.h -- host-side launchers of the gated delta rule (internal to libssm).
+#pragma once
+
+#include "launch.h"
+
+namespace ssm {
+
+// exp() of a log decay at or below this is zero in fp32; clamping there keeps
+// a full reset (g = -infinity) out of the prefix sums, where it would give NaN.
+constexpr float kMinLogDecay = -100.f;
+
+// Token-by-token path (any dtype and sizes).  `ckpt` (may be null) receives
+// the state before every kDeltaCkpt-th token of each sequence.
+constexpr int kDeltaCkpt = 32;
+// Rows of checkpoints: sequence s starts at row cu[s] / kDeltaCkpt + s, a
+// bound that holds without a prefix sum of rounded-up lengths.
+inline int64_t delta_ckpt_rows(const ssm_delta_args &a) {
+    return a.cu_seqlens ? a.seqlen / kDeltaCkpt + a.nseqs + 1
+                        : a.batch * ((a.seqlen + kDeltaCkpt - 1) / kDeltaCkpt);
+}
+cudaError_t launch_delta_simt(const ssm_delta_args &a, const SeqView &sv, float *ckpt, cudaStream_t st);
+size_t delta_simt_bwd_workspace_bytes(const ssm_delta_bwd_args &b);
+cudaError_t launch_delta_simt_bwd(const ssm_delta_bwd_args &b, const SeqView &sv, void *ws, cudaStream_t st);
+
+cudaError_t launch_delta_update(const ssm_delta_update_args &a, cudaStream_t st);
+
+}  // namespace ssm

@@ -1,0 +1,488 @@
+// delta_scan.cu -- the gated delta rule token by token in fp32 (any dtype and
+// sizes), forward and backward.
+//
+// A state row h[p, :] never meets another one:
+//     w = a_t h,  s = w . k_t,  u = beta_t (v_t[p] - s),  h = w + u k_t,
+//     y_t[p] = scale (h . q_t) = scale (w . q_t + u (k_t . q_t)),
+// so rows are spread over lanes: 8 lanes hold one row (4 consecutive states
+// of every 32), a warp holds 4 rows.  The two dot products of a token are
+// summed in one pass of 3 shuffle levels.  The chain over the tokens bounds
+// the time (about 100 ns a token: two FMA chains, the shuffles, one row of
+// shared memory), not memory; a sequence's rows run in separate CTAs.
+//
+// Backward, per row, from the last token to the first, with d = dL/dh_t:
+//     d += scale dy q;  du = d . k;  dv = beta du;  ds = -beta du;
+//     dbeta = sum_p du (v - s);  dq = scale sum_p dy h_t;
+//     dk = sum_p (u d + ds w);  d += ds k;  dg = sum_{p,n} d w;  d = a d.
+// The states before every 32nd token are kept by a forward pass; the tokens
+// between are recomputed in runs that fit in registers.  Each CTA owns 32 rows
+// and writes their share of dq, dk, dg, dbeta; a second kernel adds the shares
+// in a fixed order.
+#include "common.cuh"
+#include "delta.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRows = kWarps * 4;      // state rows per CTA
+constexpr int kTok = kDeltaCkpt;       // tokens staged at a time
+
+struct Args {
+    ssm_delta_args a;
+    SeqView sv;
+    float *ckpt;
+};
+
+// Tokens [lo, hi) of the sequence this CTA owns; row = batch row.
+struct Seq {
+    int s;
+    int64_t row, lo, hi, ckpt_row;
+};
+SSM_DEVINL Seq find_seq(const ssm_delta_args &a, const SeqView &sv, int y) {
+    Seq q;
+    if (a.cu_seqlens) {
+        q.s = sv.order[y];
+        q.row = 0;
+        q.lo = a.cu_seqlens[q.s];
+        q.hi = a.cu_seqlens[q.s + 1];
+        q.ckpt_row = q.lo / kDeltaCkpt + q.s;
+    } else {
+        q.s = y;
+        q.row = y;
+        q.lo = 0;
+        q.hi = a.seqlen;
+        q.ckpt_row = (int64_t)y * ((a.seqlen + kDeltaCkpt - 1) / kDeltaCkpt);
+    }
+    return q;
+}
+
+// State index of element e of this lane: 4 consecutive of every 32.
+SSM_DEVINL int state_of(int lane8, int e) { return (e >> 2) * 32 + lane8 * 4 + (e & 3); }
+
+// Stage `nt` tokens of a [tokens][width] operand as fp32, `pad` columns wide
+// (zeros past width and behind nt).
+template <typename T>
+SSM_DEVINL void stage(float *dst, int pad, const T *src, int64_t ts, int nt, int width) {
+    for (int i = threadIdx.x; i < kTok * pad; i += kThreads) {
+        const int t = i / pad, c = i % pad;
+        dst[i] = (t < nt && c < width) ? Elem<T>::ld(src + (int64_t)t * ts + c) : 0.f;
+    }
+}
+SSM_DEVINL float decay_of(float g) { return expf(fmaxf(g, kMinLogDecay)); }
+
+template <int NE>
+SSM_DEVINL void load_row(float (&h)[NE], const float *src, int lane8, int64_t N) {
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+        const int n = state_of(lane8, e);
+        h[e] = n < N ? src[n] : 0.f;
+    }
+}
+SSM_DEVINL float sum8(float v) {
+    v += __shfl_xor_sync(~0u, v, 1);
+    v += __shfl_xor_sync(~0u, v, 2);
+    v += __shfl_xor_sync(~0u, v, 4);
+    return v;
+}
+
+template <typename T, int NE>
+__global__ void __launch_bounds__(kThreads) delta_scan_kernel(const Args p) {
+    const ssm_delta_args &a = p.a;
+    if (p.sv.err && *p.sv.err != 0) return;
+    constexpr int NP = NE * 8;
+    extern __shared__ float sm[];
+    float *ks = sm, *qs = ks + kTok * NP, *vs = qs + kTok * NP, *as = vs + kTok * kRows, *bs = as + kTok, *kq = bs + kTok;
+    const Seq sq = find_seq(a, p.sv, blockIdx.y);
+    const int64_t H = a.nheads, P = a.headdim, N = a.dstate;
+    const int h = blockIdx.x % H, p0 = (int)(blockIdx.x / H) * kRows;
+    const int grp = (int)(h / (H / a.ngroups));
+    if (!SSM_BOUNDS(sq.hi, a.seqlen + 1, BS_DELTA_SEQ) || !SSM_BOUNDS(sq.lo, sq.hi + 1, BS_DELTA_SEQ)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lane8 = lane & 7;
+    const int r = warp * 4 + (lane >> 3);              // row within the CTA
+    const bool live = p0 + r < P;
+    const int64_t srow = ((int64_t)sq.s * H + h) * P + p0 + r;
+    float st[NE];
+    if (live && a.h0) load_row<NE>(st, a.h0 + srow * N, lane8, N);
+    else
+#pragma unroll
+        for (int e = 0; e < NE; ++e) st[e] = 0.f;
+
+    const T *q = (const T *)a.q + sq.row * a.q_batch_stride + grp * N;
+    const T *k = (const T *)a.k + sq.row * a.k_batch_stride + grp * N;
+    const T *v = (const T *)a.v + sq.row * a.v_batch_stride + h * P + p0;
+    const float *g = a.g + sq.row * a.g_batch_stride + h, *be = a.beta + sq.row * a.beta_batch_stride + h;
+    T *y = a.y ? (T *)a.y + sq.row * a.y_batch_stride + h * P + p0 : nullptr;
+    const int vw = (int)min((int64_t)kRows, P - p0);
+    for (int64_t t0 = sq.lo; t0 < sq.hi; t0 += kTok) {
+        const int nt = (int)min((int64_t)kTok, sq.hi - t0);
+        if (p.ckpt && live) {
+            float *c = p.ckpt + (((sq.ckpt_row + (t0 - sq.lo) / kDeltaCkpt) * H + h) * P + p0 + r) * N;
+#pragma unroll
+            for (int e = 0; e < NE; ++e)
+                if (state_of(lane8, e) < N) c[state_of(lane8, e)] = st[e];
+        }
+        __syncthreads();                               // the tokens before are read
+        stage(ks, NP, k + t0 * a.k_token_stride, a.k_token_stride, nt, (int)N);
+        if (y) stage(qs, NP, q + t0 * a.q_token_stride, a.q_token_stride, nt, (int)N);
+        stage(vs, kRows, v + t0 * a.v_token_stride, a.v_token_stride, nt, vw);
+        if (threadIdx.x < kTok) {
+            const int t = threadIdx.x;
+            as[t] = t < nt ? decay_of(g[(t0 + t) * a.g_token_stride]) : 1.f;
+            bs[t] = t < nt ? be[(t0 + t) * a.beta_token_stride] : 0.f;
+        }
+        __syncthreads();
+        if (y) {
+            for (int t = warp; t < nt; t += kWarps) {
+                float s = 0.f;
+                for (int n = lane; n < NP; n += 32) s = fmaf(ks[t * NP + n], qs[t * NP + n], s);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+                if (lane == 0) kq[t] = s;
+            }
+            __syncthreads();
+        }
+        for (int t = 0; t < nt; ++t) {
+            const float al = as[t];
+            float sk = 0.f, sq_ = 0.f, kk[NE];
+#pragma unroll
+            for (int e = 0; e < NE; e += 4) {
+                const float4 k4 = *reinterpret_cast<const float4 *>(ks + t * NP + state_of(lane8, e));
+                kk[e] = k4.x; kk[e + 1] = k4.y; kk[e + 2] = k4.z; kk[e + 3] = k4.w;
+            }
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                st[e] *= al;
+                sk = fmaf(st[e], kk[e], sk);
+            }
+            if (y) {
+#pragma unroll
+                for (int e = 0; e < NE; e += 4) {
+                    const float4 q4 = *reinterpret_cast<const float4 *>(qs + t * NP + state_of(lane8, e));
+                    sq_ = fmaf(st[e], q4.x, sq_);
+                    sq_ = fmaf(st[e + 1], q4.y, sq_);
+                    sq_ = fmaf(st[e + 2], q4.z, sq_);
+                    sq_ = fmaf(st[e + 3], q4.w, sq_);
+                }
+                sq_ = sum8(sq_);
+            }
+            sk = sum8(sk);
+            const float u = bs[t] * (vs[t * kRows + r] - sk);
+#pragma unroll
+            for (int e = 0; e < NE; ++e) st[e] = fmaf(u, kk[e], st[e]);
+            if (y && lane8 == 0 && live)
+                Elem<T>::st(y + (t0 + t) * a.y_token_stride + r, a.scale * fmaf(u, kq[t], sq_));
+        }
+    }
+    if (a.h_final && live) {
+        float *o = a.h_final + srow * N;
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+            if (state_of(lane8, e) < N) o[state_of(lane8, e)] = st[e];
+    }
+}
+
+// ------------------------------------------------------------------ backward
+struct BwdArgs {
+    ssm_delta_bwd_args b;
+    SeqView sv;
+    const float *ckpt;
+    float *pq, *pk;        // [slices][tokens][H][N]
+    float *pg, *pb;        // [slices][tokens][H]
+};
+
+// Sum over the 4 rows of a warp; lane group i (lanes 8i .. 8i+7) ends with a
+// quarter of the elements, NE / 4 of them: elements i * NE/4 ...
+template <int NE>
+SSM_DEVINL void rows_sum(float (&x)[NE], float (&out)[NE / 4], int lane) {
+    const bool hi = lane & 16, hi2 = lane & 8;
+    float y[NE / 2];
+#pragma unroll
+    for (int e = 0; e < NE / 2; ++e) {
+        const float give = hi ? x[e] : x[e + NE / 2], keep = hi ? x[e + NE / 2] : x[e];
+        y[e] = keep + __shfl_xor_sync(~0u, give, 16);
+    }
+#pragma unroll
+    for (int e = 0; e < NE / 4; ++e) {
+        const float give = hi2 ? y[e] : y[e + NE / 4], keep = hi2 ? y[e + NE / 4] : y[e];
+        out[e] = keep + __shfl_xor_sync(~0u, give, 8);
+    }
+}
+
+// TR tokens are held in registers at a time (TR * NE states each).
+template <typename T, int NE, int TR>
+__global__ void __launch_bounds__(kThreads, 1) delta_scan_bwd_kernel(const BwdArgs p) {
+    const ssm_delta_args &a = p.b.fwd;
+    if (p.sv.err && *p.sv.err != 0) return;
+    constexpr int NP = NE * 8;
+    extern __shared__ float sm[];
+    float *ks = sm, *qs = ks + kTok * NP, *vs = qs + kTok * NP, *ds_ = vs + kTok * kRows, *as = ds_ + kTok * kRows,
+          *bs = as + kTok;
+    float *rq = bs + kTok;                     // [TR][kWarps][NP] each
+    float *rk = rq + TR * kWarps * NP;
+    float *rg = rk + TR * kWarps * NP;         // [TR][kWarps]
+    float *rb = rg + TR * kWarps;
+    const Seq sq = find_seq(a, p.sv, blockIdx.y);
+    const int64_t H = a.nheads, P = a.headdim, N = a.dstate;
+    const int h = blockIdx.x % H, slice = (int)(blockIdx.x / H), p0 = slice * kRows;
+    const int grp = (int)(h / (H / a.ngroups));
+    if (!SSM_BOUNDS(sq.hi, a.seqlen + 1, BS_DELTA_SEQ) || !SSM_BOUNDS(sq.lo, sq.hi + 1, BS_DELTA_SEQ)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lane8 = lane & 7;
+    const int r = warp * 4 + (lane >> 3);
+    const bool live = p0 + r < P;
+    const int64_t srow = ((int64_t)sq.s * H + h) * P + p0 + r;
+    float d[NE];
+    if (live && p.b.dh_final) load_row<NE>(d, p.b.dh_final + srow * N, lane8, N);
+    else
+#pragma unroll
+        for (int e = 0; e < NE; ++e) d[e] = 0.f;
+    const T *q = (const T *)a.q + sq.row * a.q_batch_stride + grp * N;
+    const T *k = (const T *)a.k + sq.row * a.k_batch_stride + grp * N;
+    const T *v = (const T *)a.v + sq.row * a.v_batch_stride + h * P + p0;
+    const T *dy = (const T *)p.b.dy + sq.row * p.b.dy_batch_stride + h * P + p0;
+    const float *g = a.g + sq.row * a.g_batch_stride + h, *be = a.beta + sq.row * a.beta_batch_stride + h;
+    const int64_t tok0 = sq.row * a.seqlen;    // tokens of all rows are numbered through in the outputs
+    const int64_t ntok = a.batch * a.seqlen;
+    T *dv = (T *)p.b.dv + h * P + p0;
+    const int vw = (int)min((int64_t)kRows, P - p0);
+
+    const int64_t len = sq.hi - sq.lo;
+    for (int64_t c = (len + kTok - 1) / kTok - 1; c >= 0; --c) {
+        const int64_t t0 = sq.lo + c * kTok;
+        const int nt = (int)min((int64_t)kTok, sq.hi - t0);
+        __syncthreads();
+        stage(ks, NP, k + t0 * a.k_token_stride, a.k_token_stride, nt, (int)N);
+        stage(qs, NP, q + t0 * a.q_token_stride, a.q_token_stride, nt, (int)N);
+        stage(vs, kRows, v + t0 * a.v_token_stride, a.v_token_stride, nt, vw);
+        stage(ds_, kRows, dy + t0 * p.b.dy_token_stride, p.b.dy_token_stride, nt, vw);
+        if (threadIdx.x < kTok) {
+            const int t = threadIdx.x;
+            as[t] = t < nt ? decay_of(g[(t0 + t) * a.g_token_stride]) : 1.f;
+            bs[t] = t < nt ? be[(t0 + t) * a.beta_token_stride] : 0.f;
+        }
+        __syncthreads();
+        const float *cp = p.ckpt + (((sq.ckpt_row + c) * H + h) * P + p0 + r) * N;
+        for (int run = (nt + TR - 1) / TR - 1; run >= 0; --run) {
+            float st[NE];
+            if (live) load_row<NE>(st, cp, lane8, N);
+            else
+#pragma unroll
+                for (int e = 0; e < NE; ++e) st[e] = 0.f;
+            // forward to the run's first token
+            for (int t = 0; t < run * TR; ++t) {
+                float sk = 0.f;
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    st[e] *= as[t];
+                    sk = fmaf(st[e], ks[t * NP + state_of(lane8, e)], sk);
+                }
+                const float u = bs[t] * (vs[t * kRows + r] - sum8(sk));
+#pragma unroll
+                for (int e = 0; e < NE; ++e) st[e] = fmaf(u, ks[t * NP + state_of(lane8, e)], st[e]);
+            }
+            // through the run: w = a h_{t-1} of every token stays in registers
+            float w[TR][NE], uu[TR], sk_[TR];
+#pragma unroll
+            for (int i = 0; i < TR; ++i) {
+                const int t = run * TR + i;                    // t < kTok; tokens behind nt have a = 1, beta = 0
+                float sk = 0.f;
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    w[i][e] = st[e] * as[t];
+                    sk = fmaf(w[i][e], ks[t * NP + state_of(lane8, e)], sk);
+                }
+                sk_[i] = sum8(sk);
+                uu[i] = bs[t] * (vs[t * kRows + r] - sk_[i]);
+#pragma unroll
+                for (int e = 0; e < NE; ++e) st[e] = fmaf(uu[i], ks[t * NP + state_of(lane8, e)], w[i][e]);
+            }
+#pragma unroll
+            for (int i = TR - 1; i >= 0; --i) {
+                const int t = run * TR + i;
+                const float dyv = a.scale * ds_[t * kRows + r];
+                float x[NE], part[NE / 4], du = 0.f;
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    const int n = t * NP + state_of(lane8, e);
+                    x[e] = dyv * fmaf(uu[i], ks[n], w[i][e]);          // dq: dy h_t
+                    d[e] = fmaf(dyv, qs[n], d[e]);
+                    du = fmaf(d[e], ks[n], du);
+                }
+                du = sum8(du);
+                rows_sum<NE>(x, part, lane);
+                // lanes 8i .. 8i+7 hold elements of quarter ((lane>>4)&1)*2 + ((lane>>3)&1)
+                const int q4 = ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1);
+#pragma unroll
+                for (int e = 0; e < NE / 4; ++e) rq[(i * kWarps + warp) * NP + state_of(lane8, q4 * (NE / 4) + e)] = part[e];
+                const float dsv = -bs[t] * du;
+                float dg = 0.f;
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    const int n = t * NP + state_of(lane8, e);
+                    x[e] = fmaf(uu[i], d[e], dsv * w[i][e]);
+                    d[e] = fmaf(dsv, ks[n], d[e]);
+                    dg = fmaf(d[e], w[i][e], dg);
+                    d[e] *= as[t];
+                }
+                rows_sum<NE>(x, part, lane);
+#pragma unroll
+                for (int e = 0; e < NE / 4; ++e) rk[(i * kWarps + warp) * NP + state_of(lane8, q4 * (NE / 4) + e)] = part[e];
+                float db = lane8 == 0 ? du * (vs[t * kRows + r] - sk_[i]) : 0.f;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) {
+                    dg += __shfl_xor_sync(~0u, dg, o);
+                    db += __shfl_xor_sync(~0u, db, o);
+                }
+                if (lane == 0) {
+                    rg[i * kWarps + warp] = dg;
+                    rb[i * kWarps + warp] = db;
+                }
+                if (lane8 == 0 && live && t < nt)
+                    Elem<T>::st(dv + (tok0 + t0 + t) * H * P + r, -dsv);
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < TR * NP; i += kThreads) {
+                const int ti = i / NP, n = i % NP, t = run * TR + ti;
+                if (t >= nt || n >= N) continue;
+                float sqv = 0.f, skv = 0.f;
+#pragma unroll
+                for (int wv = 0; wv < kWarps; ++wv) {
+                    sqv += rq[(ti * kWarps + wv) * NP + n];
+                    skv += rk[(ti * kWarps + wv) * NP + n];
+                }
+                const int64_t at = (((int64_t)slice * ntok + tok0 + t0 + t) * H + h) * N + n;
+                p.pq[at] = sqv;
+                p.pk[at] = skv;
+            }
+            if (threadIdx.x < TR && run * TR + (int)threadIdx.x < nt) {
+                const int ti = threadIdx.x;
+                float sg = 0.f, sb = 0.f;
+#pragma unroll
+                for (int wv = 0; wv < kWarps; ++wv) {
+                    sg += rg[ti * kWarps + wv];
+                    sb += rb[ti * kWarps + wv];
+                }
+                const int64_t at = ((int64_t)slice * ntok + tok0 + t0 + run * TR + ti) * H + h;
+                p.pg[at] = sg;
+                p.pb[at] = sb;
+            }
+            __syncthreads();
+        }
+    }
+    if (p.b.dh0 && live) {
+        float *o = p.b.dh0 + srow * N;
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+            if (state_of(lane8, e) < N) o[state_of(lane8, e)] = d[e];
+    }
+}
+
+// Adds the shares of the row slices and, for dq / dk, of a group's heads.
+template <typename T>
+__global__ void delta_shares_kernel(const BwdArgs p, int slices) {
+    if (p.sv.err && *p.sv.err != 0) return;
+    const ssm_delta_args &a = p.b.fwd;
+    const int64_t H = a.nheads, N = a.dstate, G = a.ngroups, R = H / G, ntok = a.batch * a.seqlen;
+    const int64_t stride = (int64_t)gridDim.x * blockDim.x, first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    for (int64_t i = first; i < ntok * G * N; i += stride) {
+        const int64_t n = i % N, gt = i / N, grp = gt % G, t = gt / G;
+        float sq = 0.f, sk = 0.f;
+        for (int s = 0; s < slices; ++s)
+            for (int64_t j = 0; j < R; ++j) {
+                const int64_t at = (((int64_t)s * ntok + t) * H + grp * R + j) * N + n;
+                sq += p.pq[at];
+                sk += p.pk[at];
+            }
+        Elem<T>::st((T *)p.b.dq + i, sq);
+        Elem<T>::st((T *)p.b.dk + i, sk);
+    }
+    for (int64_t i = first; i < ntok * H; i += stride) {
+        float sg = 0.f, sb = 0.f;
+        for (int s = 0; s < slices; ++s) {
+            sg += p.pg[(int64_t)s * ntok * H + i];
+            sb += p.pb[(int64_t)s * ntok * H + i];
+        }
+        Elem<T>::st((T *)p.b.dg + i, sg);
+        Elem<T>::st((T *)p.b.dbeta + i, sb);
+    }
+}
+
+template <typename K>
+cudaError_t set_smem(K kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T, int NE>
+cudaError_t run_fwd(const Args &p, dim3 grid, cudaStream_t st) {
+    const size_t smem = (size_t)(2 * kTok * NE * 8 + kTok * kRows + 3 * kTok) * 4;
+    cudaError_t e = set_smem(delta_scan_kernel<T, NE>, smem);
+    if (e != cudaSuccess) return e;
+    delta_scan_kernel<T, NE><<<grid, kThreads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+template <typename T, int NE, int TR>
+cudaError_t run_bwd(const BwdArgs &p, dim3 grid, cudaStream_t st) {
+    const size_t smem =
+        (size_t)(2 * kTok * NE * 8 + 2 * kTok * kRows + 2 * kTok + 2 * TR * kWarps * NE * 8 + 2 * TR * kWarps) * 4;
+    cudaError_t e = set_smem(delta_scan_bwd_kernel<T, NE, TR>, smem);
+    if (e != cudaSuccess) return e;
+    delta_scan_bwd_kernel<T, NE, TR><<<grid, kThreads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+int64_t slices_of(const ssm_delta_args &a) { return (a.headdim + kRows - 1) / kRows; }
+int64_t seqs_of(const ssm_delta_args &a) { return a.cu_seqlens ? a.nseqs : a.batch; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+cudaError_t launch_delta_simt(const ssm_delta_args &a, const SeqView &sv, float *ckpt, cudaStream_t st) {
+    if (seqs_of(a) == 0) return cudaSuccess;
+    const Args p{a, sv, ckpt};
+    const dim3 grid((unsigned)(a.nheads * slices_of(a)), (unsigned)seqs_of(a));
+    const bool bf = a.dtype == SSM_BF16;
+    if (a.dstate <= 64) return bf ? run_fwd<__nv_bfloat16, 8>(p, grid, st) : run_fwd<float, 8>(p, grid, st);
+    if (a.dstate <= 128) return bf ? run_fwd<__nv_bfloat16, 16>(p, grid, st) : run_fwd<float, 16>(p, grid, st);
+    return bf ? run_fwd<__nv_bfloat16, 32>(p, grid, st) : run_fwd<float, 32>(p, grid, st);
+}
+
+size_t delta_simt_bwd_workspace_bytes(const ssm_delta_bwd_args &b) {
+    const ssm_delta_args &a = b.fwd;
+    const size_t tok = (size_t)(a.batch * a.seqlen) * a.nheads * slices_of(a) * 4;
+    return up256((size_t)delta_ckpt_rows(a) * a.nheads * a.headdim * a.dstate * 4) + 2 * up256(tok * a.dstate) +
+           2 * up256(tok);
+}
+
+cudaError_t launch_delta_simt_bwd(const ssm_delta_bwd_args &b, const SeqView &sv, void *ws, cudaStream_t st) {
+    const ssm_delta_args &a = b.fwd;
+    if (seqs_of(a) == 0) return cudaSuccess;
+    char *w = static_cast<char *>(ws);
+    float *ckpt = reinterpret_cast<float *>(w);
+    w += up256((size_t)delta_ckpt_rows(a) * a.nheads * a.headdim * a.dstate * 4);
+    const size_t tok = (size_t)(a.batch * a.seqlen) * a.nheads * slices_of(a) * 4;
+    BwdArgs p{b, sv, ckpt, nullptr, nullptr, nullptr, nullptr};
+    p.pq = reinterpret_cast<float *>(w); w += up256(tok * a.dstate);
+    p.pk = reinterpret_cast<float *>(w); w += up256(tok * a.dstate);
+    p.pg = reinterpret_cast<float *>(w); w += up256(tok);
+    p.pb = reinterpret_cast<float *>(w);
+    ssm_delta_args f = a;
+    f.y = nullptr;
+    f.h_final = nullptr;
+    cudaError_t e = launch_delta_simt(f, sv, ckpt, st);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(a.nheads * slices_of(a)), (unsigned)seqs_of(a));
+    const bool bf = a.dtype == SSM_BF16;
+    if (a.dstate <= 64) e = bf ? run_bwd<__nv_bfloat16, 8, 8>(p, grid, st) : run_bwd<float, 8, 8>(p, grid, st);
+    else if (a.dstate <= 128) e = bf ? run_bwd<__nv_bfloat16, 16, 8>(p, grid, st) : run_bwd<float, 16, 8>(p, grid, st);
+    else e = bf ? run_bwd<__nv_bfloat16, 32, 4>(p, grid, st) : run_bwd<float, 32, 4>(p, grid, st);
+    if (e != cudaSuccess) return e;
+    const int64_t work = a.batch * a.seqlen * a.ngroups * a.dstate;
+    if (work == 0) return cudaSuccess;
+    const int blocks = (int)min((work + 255) / 256, (int64_t)sm_count() * 8);
+    if (bf) delta_shares_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(p, (int)slices_of(a));
+    else delta_shares_kernel<float><<<blocks, 256, 0, st>>>(p, (int)slices_of(a));
+    return cudaGetLastError();
+}
+
+}  // namespace ssm

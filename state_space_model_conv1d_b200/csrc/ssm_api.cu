@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/ssm.h"
+#include "api_util.h"
 #include "common.cuh"
 #include "launch.h"
 
@@ -14,36 +15,25 @@ __device__ BoundsRecord g_ssm_bounds;
 }
 #endif
 
+namespace ssm {
 namespace {
-
 thread_local int32_t g_last_cuda_error = 0;
-
+}
 ssm_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return SSM_OK;
     g_last_cuda_error = (int32_t)e;
     return SSM_ERR_CUDA;
 }
+int32_t last_cuda_error() { return g_last_cuda_error; }
+}  // namespace ssm
 
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-size_t esize(int32_t dtype) { return dtype == SSM_BF16 ? 2 : 4; }
-bool dtype_ok(int32_t d) { return d == SSM_F32 || d == SSM_BF16; }
+namespace {
 
-// A token-major activation: row width w elements, strides in elements.
-ssm_status check_act(const void *p, int64_t bs, int64_t ts, int64_t w, int64_t batch, int64_t seqlen, size_t es,
-                     bool required) {
-    if (!p) return required ? SSM_ERR_INVALID_ARG : SSM_OK;
-    if (!aligned(p, es)) return SSM_ERR_ALIGNMENT;
-    if (ts < 0 || bs < 0) return SSM_ERR_INVALID_ARG;
-    if (seqlen > 1 && ts < w) return SSM_ERR_INVALID_ARG;          // token rows may not overlap
-    if (batch > 1 && bs < ts * (seqlen - 1) + w) return SSM_ERR_INVALID_ARG;
-    return SSM_OK;
-}
-
-#define SSM_TRY(expr)                      \
-    do {                                   \
-        ssm_status st_ = (expr);           \
-        if (st_ != SSM_OK) return st_;     \
-    } while (0)
+using ssm::aligned;
+using ssm::check_act;
+using ssm::cuda_status;
+using ssm::dtype_ok;
+using ssm::esize;
 
 ssm_status validate_conv(const ssm_conv_args *a) {
     if (!a) return SSM_ERR_INVALID_ARG;
@@ -168,7 +158,7 @@ const char *ssm_status_string(ssm_status s) {
     return "unknown status";
 }
 
-int32_t ssm_last_cuda_error(void) { return g_last_cuda_error; }
+int32_t ssm_last_cuda_error(void) { return ssm::last_cuda_error(); }
 
 ssm_status ssm_conv1d_fwd(const ssm_conv_args *args, void *stream) {
     SSM_TRY(validate_conv(args));
