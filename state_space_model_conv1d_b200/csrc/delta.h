@@ -22,6 +22,13 @@ cudaError_t launch_delta_simt(const ssm_delta_args &a, const SeqView &sv, float 
 size_t delta_simt_bwd_workspace_bytes(const ssm_delta_bwd_args &b);
 cudaError_t launch_delta_simt_bwd(const ssm_delta_bwd_args &b, const SeqView &sv, void *ws, cudaStream_t st);
 
+// Tensor-core path in blocks of 64 tokens: the shapes it takes (they decide the
+// workspace), the pointers and strides it needs besides, and its launcher.
+bool delta_tc_shape(const ssm_delta_args &a);
+bool delta_tc_ok(const ssm_delta_args &a);
+size_t delta_tc_workspace_bytes(const ssm_delta_args &a);
+cudaError_t launch_delta_tc(const ssm_delta_args &a, const SeqView &sv, void *ws, cudaStream_t st);
+
 cudaError_t launch_delta_update(const ssm_delta_update_args &a, cudaStream_t st);
 
 }  // namespace ssm

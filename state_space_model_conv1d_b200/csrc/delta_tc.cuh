@@ -1,0 +1,171 @@
+// delta_tc.cuh -- pieces shared by the tensor-core kernels of the gated delta
+// rule: block geometry, bounded waits, tensor-memory helpers, gate tables.
+#pragma once
+
+#include "common.cuh"
+#include "delta.h"
+#include "tc05.cuh"
+
+namespace ssm {
+namespace dtc {
+
+constexpr int kQ = 64;                    // tokens per block
+constexpr uint32_t kTile = 8192;          // 64 rows x 64 bf16: one 128-byte-swizzled tile
+constexpr size_t kTBytes = 2 * kTile;     // T of one (block, head): high and low parts
+
+// Wait for an mbarrier phase, at most two seconds; gives up as soon as another
+// thread of the CTA has (`abort`), and records the timeout in the error word.
+SSM_DEVINL bool wait_bar(uint64_t *mb, volatile int *abort, uint32_t parity, int32_t *err) {
+    if (tc::mbar_try_wait(mb, parity)) return true;
+    const uint64_t t0 = tc::globaltimer_ns();
+    for (;;) {
+        if (*abort) return false;
+        if (tc::mbar_try_wait(mb, parity)) return true;
+        if (tc::globaltimer_ns() - t0 > 2000000000ull) break;
+    }
+    *abort = 1;
+    if (err) atomicExch(err, SSM_DEVERR_TIMEOUT);
+    return false;
+}
+SSM_DEVINL void arrive(uint64_t *mbar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_u32(mbar)) : "memory");
+}
+
+// A operand in tensor memory (row = lane, two bf16 of K per column); `skip`:
+// lanes of the accumulator to leave alone, 32 per word.
+SSM_DEVINL void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+SSM_DEVINL void mma_ts_lanes(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t skip_lo,
+                             uint32_t skip_hi) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %6, %6}, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(skip_lo), "r"(skip_hi));
+}
+
+SSM_DEVINL void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+SSM_DEVINL void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+    tmem_st16(taddr, r);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[16 + i]);
+    tmem_st16(taddr + 16, r);
+}
+SSM_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// Two bf16 parts of a float: high = nearest bf16, low = nearest bf16 of the
+// rest; together 16 bits of mantissa, relative error at most 2^-17.
+SSM_DEVINL uint32_t pack2(float a, float b) {
+    __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&p);
+}
+SSM_DEVINL void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = pack2(a, b);
+    lo = pack2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+}
+SSM_DEVINL void split32(const float (&v)[32], uint32_t (&hi)[16], uint32_t (&lo)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) split2(v[2 * i], v[2 * i + 1], hi[i], lo[i]);
+}
+
+// cp.async.bulk of a contiguous range, global -> shared.
+SSM_DEVINL void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *mbar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+            tc::smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(tc::smem_u32(mbar))
+        : "memory");
+}
+SSM_DEVINL void tma_load_4d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, uint64_t *mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];\n" ::"r"(tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(tc::smem_u32(mbar))
+        : "memory");
+}
+
+// Byte offset of (row, col) in a 64-row tile of 64 bf16 columns, 128-byte swizzle.
+SSM_DEVINL uint32_t swz(int row, int col) {
+    return (uint32_t)row * 128u + ((uint32_t)((col >> 3) ^ (row & 7)) << 4) + (uint32_t)(col & 7) * 2u;
+}
+
+// Prefix sums of the log decays of one block, by one warp: lane l holds tokens
+// l and l + 32.  In 64 bits, because the decays between tokens are differences
+// of sums that may be far from zero; tokens behind the sequence's end count 0.
+SSM_DEVINL void block_cs(float g0, float g1, double &c0, double &c1, double &last) {
+    const int lane = threadIdx.x & 31;
+    c0 = g0;
+    c1 = g1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(~0u, c0, o), y = __shfl_up_sync(~0u, c1, o);
+        if (lane >= o) {
+            c0 += x;
+            c1 += y;
+        }
+    }
+    c1 += __shfl_sync(~0u, c0, 31);
+    last = __shfl_sync(~0u, c1, 31);
+}
+SSM_DEVINL float exp_d(double x) { return ex2((float)(x * 1.4426950408889634)); }
+
+// The sequence and block of a packed slot (see delta_slot below); c < 0: none.
+struct Block {
+    int s;          // sequence
+    int64_t row;    // batch row
+    int64_t t0;     // first token (within the row)
+    int nt;         // tokens, 0: empty slot
+};
+SSM_DEVINL int64_t seq_slot(const int32_t *cu, int s, int64_t nblk) {
+    return cu ? (int64_t)cu[s] / kQ + s : (int64_t)s * nblk;
+}
+SSM_DEVINL Block find_block(const int32_t *cu, int nseqs, int64_t seqlen, int64_t nblk, int64_t slot) {
+    Block b;
+    int64_t lo, hi, c;
+    if (cu) {
+        int l = 0, h = nseqs - 1;
+        while (l < h) {
+            const int m = (l + h + 1) >> 1;
+            if ((int64_t)cu[m] / kQ + m <= slot) l = m;
+            else h = m - 1;
+        }
+        b.s = l;
+        b.row = 0;
+        lo = cu[l];
+        hi = cu[l + 1];
+        c = slot - ((int64_t)cu[l] / kQ + l);
+    } else {
+        b.s = (int)(slot / nblk);
+        b.row = b.s;
+        lo = 0;
+        hi = seqlen;
+        c = slot % nblk;
+    }
+    b.t0 = lo + c * kQ;
+    b.nt = (int)max((int64_t)0, min((int64_t)kQ, hi - b.t0));
+    return b;
+}
+
+}  // namespace dtc
+
+// Slots of per-block data: sequence s starts at slot cu[s] / 64 + s (a bound
+// that needs no prefix sum over rounded-up lengths), batch row r at r * blocks.
+inline int64_t delta_blocks_per_row(const ssm_delta_args &a) { return (a.seqlen + dtc::kQ - 1) / dtc::kQ; }
+inline int64_t delta_slots(const ssm_delta_args &a) {
+    return a.cu_seqlens ? a.seqlen / dtc::kQ + a.nseqs + 1 : a.batch * delta_blocks_per_row(a);
+}
+
+}  // namespace ssm

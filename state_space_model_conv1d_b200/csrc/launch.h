@@ -86,6 +86,10 @@ cudaError_t launch_ssd(const ssm_scan_args &a, const SeqView &sv, void *ws_bc, c
 // TMA map with a 64-channel x box_rows-token box (128-byte swizzle or none).
 bool make_map_box(CUtensorMap *m, const void *base, int64_t channels, int64_t tokens, int64_t batch, int64_t ts,
                   int64_t bs, bool swizzle, int box_rows);
+// A [batch][tokens][groups][n] bf16 tensor as a 4-d map with 64 n x 64-token boxes of one
+// group (128-byte swizzle): columns past n read as zeros.
+bool make_map_group(CUtensorMap *m, const void *base, int64_t n, int64_t groups, int64_t tokens, int64_t batch,
+                    int64_t ts, int64_t bs);
 cudaError_t launch_state_update(const ssm_update_args &a, cudaStream_t st);
 // Backward scan: workspace bytes for the checkpoints and B / C accumulators
 // (after the error word and the varlen order), and its launcher.

@@ -123,7 +123,7 @@ extern "C" {
 
 size_t ssm_delta_workspace_size(const ssm_delta_args *args) {
     if (!args || !sizes_ok(*args)) return 0;
-    return delta_prefix(*args);
+    return delta_prefix(*args) + (ssm::delta_tc_shape(*args) ? ssm::delta_tc_workspace_bytes(*args) : 0);
 }
 
 ssm_status ssm_delta_fwd(const ssm_delta_args *args, void *workspace, size_t ws_bytes, void *stream) {
@@ -131,7 +131,9 @@ ssm_status ssm_delta_fwd(const ssm_delta_args *args, void *workspace, size_t ws_
     const cudaStream_t st = (cudaStream_t)stream;
     if (!workspace || ws_bytes < ssm_delta_workspace_size(args) || !aligned(workspace, 256)) return SSM_ERR_WORKSPACE;
     ssm::SeqView sv;
-    SSM_TRY(delta_plan(*args, static_cast<char *>(workspace), st, &sv));
+    char *ws = static_cast<char *>(workspace);
+    SSM_TRY(delta_plan(*args, ws, st, &sv));
+    if (ssm::delta_tc_ok(*args)) return cuda_status(ssm::launch_delta_tc(*args, sv, ws + delta_prefix(*args), st));
     return cuda_status(ssm::launch_delta_simt(*args, sv, nullptr, st));
 }
 

@@ -1519,6 +1519,19 @@ bool make_map_box(CUtensorMap *m, const void *base, int64_t channels, int64_t to
                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+bool make_map_group(CUtensorMap *m, const void *base, int64_t n, int64_t groups, int64_t tokens, int64_t batch,
+                    int64_t ts, int64_t bs) {
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)n, (cuuint64_t)groups, (cuuint64_t)tokens, (cuuint64_t)batch};
+    const cuuint64_t strides[3] = {(cuuint64_t)n * 2, (cuuint64_t)(tokens > 1 ? ts : n * groups) * 2,
+                                   (cuuint64_t)(batch > 1 ? bs : (tokens > 1 ? ts : n * groups) * tokens) * 2};
+    const cuuint32_t box[4] = {64, 1, 64, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 bool make_map(CUtensorMap *m, const void *base, int64_t channels, int64_t tokens, int64_t batch, int64_t ts, int64_t bs,
               bool swizzle) {
     return make_map_box(m, base, channels, tokens, batch, ts, bs, swizzle, kQ);
