@@ -1,18 +1,26 @@
-// delta_prep.cu -- the triangular inverse behind the blocked gated delta rule.
+// delta_prep.cu -- what the blocked gated delta rule needs of every (block,
+// head) and what does not depend on the state: the triangular inverse T and
+// the attention weights.
 //
 // Within a block of 64 tokens, with cs the inclusive prefix sum of the log
 // decays and h the state entering the block,
 //     u_i = beta_i (v_i - exp(cs_i) h k_i - sum_{j<i} exp(cs_i - cs_j) (k_i . k_j) u_j),
 // so U = T R with R_i = beta_i (v_i - exp(cs_i) h k_i), T = (I + M)^-1 and
-// M_ij = beta_i exp(cs_i - cs_j) (k_i . k_j) below the diagonal.
+// M_ij = beta_i exp(cs_i - cs_j) (k_i . k_j) below the diagonal; the output
+// needs P_ij = scale exp(cs_i - cs_j) (q_i . k_j) up to it.
 //
-// One CTA per (block, heads of one group): K K^T once on mma.sync for all the
-// heads (bf16 operands are exact, so the products are), then per head M in
-// fp32, the four 16 x 16 diagonal blocks by forward substitution (stable
-// however alike the keys are, which a series in powers of M is not), and the
-// blocks below by T_ij = -T_ii sum_k M_ik T_kj, warp j keeping column j in
-// registers: tf32 products with each factor in two parts, about fp32.  T goes
-// out as two bf16 parts in the layout the tensor-core kernels read.
+// One CTA per (block, heads of one group), four warps.  [K; Q] K^T is one
+// group of tcgen05 MMAs for all the heads and stays in tensor memory, a row in
+// each lane.  Then, two heads at a time, warps 2 and 3 make P and warps 0 and
+// 1 make M (fp32, shared memory) and invert one head each: lane = column, both
+// 32 x 32 diagonal blocks by forward substitution side by side (stable however
+// alike the keys are, which a series in powers of M is not), then
+// T21 = -T22 (M21 T11).  Rows of M and T22 are read by all lanes at once as 16
+// bytes and multiplied two columns at a time.  T goes out as two bf16 parts
+// and P as bf16, both in the swizzled layout that the chain's operands have.
+// Bound by latency and issue slots (about 3000 instructions per inverse).
+#include <string.h>
+
 #include "delta_tc.cuh"
 
 namespace ssm {
@@ -20,234 +28,324 @@ namespace {
 
 using namespace dtc;
 
-constexpr int kLd = 68;                    // row of an fp32 64 x 64 tile
+constexpr int kLd = 68;                    // row of an fp32 64 x 64 tile (16-byte aligned, 4 banks further each row)
+constexpr int kPair = 2;                   // heads in work at a time
 
 struct PrepArgs {
-    const __nv_bfloat16 *k;
-    int64_t k_bs, k_ts;
     const float *g, *beta;
     int64_t g_bs, g_ts, b_bs, b_ts;
     const int32_t *cu;
-    const int32_t *err;
-    int nseqs, H, G, N, heads_per_cta;
+    int32_t *err;
+    int nseqs, H, G, heads_per_cta;
     int64_t seqlen, nblk;
-    uint8_t *T;                            // [slot][H][kTBytes]
+    float scale;
+    uint8_t *out;                          // [slot][H][kHeadBytes]
 };
 
+struct Gates {
+    float hi[kQ], lo[kQ], beta[kQ];        // prefix sums in two parts
+};
+struct Head {
+    float m[kQ * kLd];                     // M, then T22 in its place and T's high part over the first rows
+    uint8_t lo[kTile];                     // T's low part
+};
 struct PrepSmem {
-    uint8_t k[2 * kTile];
-    float m[kQ * kLd], t[kQ * kLd];
-    float hi[kQ], lo[kQ], beta[kQ];
+    union {
+        uint8_t kq[4 * kTile];             // per 64-column atom: K rows, Q rows
+        Head head[kPair];
+    };
+    Gates gates[kPair];
+    uint64_t mb;
+    uint32_t tmem;
+    int abort;
 };
 
-SSM_DEVINL void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-SSM_DEVINL void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-SSM_DEVINL void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-SSM_DEVINL void tf32_parts(float x, uint32_t &hi, uint32_t &lo) {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+// Bulk copy shared -> global of this warp's own writes (one thread), and the wait until it has read them.
+SSM_DEVINL void bulk_store(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(tc::smem_u32(src)),
+                 "r"(bytes)
+                 : "memory");
 }
 
-// acc[2 column tiles][4] += A B for 16 x 16 blocks.  A is an accumulator
-// fragment (element (g, 8 s + 2 t + e) of k-step s, g = lane / 4, t = lane % 4):
-// read as an A fragment its k index t stands for column 2 t and t + 4 for
-// 2 t + 1, so B is loaded with its rows in that order.  B[k][n] = b[n][k].
-SSM_DEVINL void mul16(float (&acc)[2][4], const float (&a)[2][4], const float *b, int g, int t) {
+// acc = sum over k < 4 n4 of row[k] x[k], two columns at a time.
+template <int N4>
+SSM_DEVINL float dot_row(const float *row, const float2 *x) {
+    float2 a0 = make_float2(0.f, 0.f), a1 = a0;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        uint32_t ah[4], al[4];
-        tf32_parts(a[s][0], ah[0], al[0]);
-        tf32_parts(a[s][2], ah[1], al[1]);
-        tf32_parts(a[s][1], ah[2], al[2]);
-        tf32_parts(a[s][3], ah[3], al[3]);
+    for (int k = 0; k < N4; ++k) {
+        const float4 u = *reinterpret_cast<const float4 *>(row + 4 * k);
+        a0 = __ffma2_rn(make_float2(u.x, u.y), x[2 * k], a0);
+        a1 = __ffma2_rn(make_float2(u.z, u.w), x[2 * k + 1], a1);
+    }
+    return (a0.x + a0.y) + (a1.x + a1.y);
+}
+
+// T = (I + M)^-1 of one head, in place, then as two bf16 parts, by two warps
+// (`part` 0, 1; they meet at barrier `bar`).  The loops are short on purpose:
+// unrolled altogether they would leave the instruction cache.
+SSM_DEVINL void invert(Head &hd, int lane, int part, int bar) {
+    float *m = hd.m;
+    const int c = lane & 15, up = lane >> 4;
+    const auto meet = [&] { asm volatile("bar.sync %0, 64;\n" ::"r"(bar) : "memory"); };
+    {   // the 32 x 32 diagonal block `part`: its two 16 x 16 blocks (half a warp each, lane = column) by forward
+        // substitution; M is zero at and above the diagonal, and so are the x not known yet
+        float *d0 = m + 32 * part * (kLd + 1), *d = d0 + 16 * up * (kLd + 1);
+        float2 x[8];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const float2 v = *reinterpret_cast<const float2 *>(b + (8 * n + g) * kLd + 8 * s + 2 * t);
-            uint32_t h0, l0, h1, l1;
-            tf32_parts(v.x, h0, l0);
-            tf32_parts(v.y, h1, l1);
-            mma1688(acc[n], al, h0, h1);
-            mma1688(acc[n], ah, l0, l1);
-            mma1688(acc[n], ah, h0, h1);
+        for (int k = 0; k < 8; ++k) x[k] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+#pragma unroll
+            for (int k = 0; k < i; k += 4) {
+                const float4 u = *reinterpret_cast<const float4 *>(d + i * kLd + k);
+                a0 = __ffma2_rn(make_float2(u.x, u.y), x[k / 2], a0);
+                a1 = __ffma2_rn(make_float2(u.z, u.w), x[k / 2 + 1], a1);
+            }
+            const float v = (i == c ? 1.f : 0.f) - ((a0.x + a0.y) + (a1.x + a1.y));
+            if (i & 1) x[i / 2].y = v;
+            else x[i / 2].x = v;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) d[i * kLd + c] = i & 1 ? x[i / 2].y : x[i / 2].x;
+        __syncwarp();
+        // the block below the first: T21 = -T22 (M21 T11), a column of T11 in each lane of half a warp, rows split
+        if (up)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = make_float2(d0[2 * k * kLd + c], d0[(2 * k + 1) * kLd + c]);
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+            const float *a = d0 + 16 * kLd + (pass ? 16 : 0);
+            float z[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = dot_row<4>(a + (8 * up + i) * kLd, x);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d0[(16 + 8 * up + i) * kLd + c] = pass ? -z[i] : z[i];
+            __syncwarp();
+            if (pass == 0)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    x[k] = make_float2(d0[(16 + 2 * k) * kLd + c], d0[(17 + 2 * k) * kLd + c]);
         }
     }
+    meet();
+    // the 32 x 32 block below: lane = column, 16 rows per warp
+    float2 x[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = make_float2(m[2 * k * kLd + lane], m[(2 * k + 1) * kLd + lane]);
+    const int r0 = 32 + 16 * part;
+#pragma unroll 1
+    for (int i = r0; i < r0 + 16; i += 4) {
+        float z[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = dot_row<8>(m + (i + e) * kLd, x);
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[(i + e) * kLd + lane] = z[e];
+    }
+    // The high part of T lies over the fp32 rows: row i of it ends at byte 128 (i + 1), row j of those begins at
+    // 272 j, so T's rows 0 - 31 (first warp, in order) only meet fp32 rows that are read, and rows 32 - 63 end
+    // before fp32 row 32.
+    uint8_t *hi = reinterpret_cast<uint8_t *>(m), *lo = hd.lo;
+    const auto put = [&](int i, int j, float v) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+        *reinterpret_cast<__nv_bfloat16 *>(hi + swz(i, j)) = h;
+        *reinterpret_cast<__nv_bfloat16 *>(lo + swz(i, j)) = __float2bfloat16_rn(v - __bfloat162float(h));
+    };
+    meet();                                            // the products are written, T11 is read
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = make_float2(m[(32 + 2 * k) * kLd + lane], m[(33 + 2 * k) * kLd + lane]);
+    if (part == 0)
+#pragma unroll 1
+        for (int i = 0; i < 32; i += 4) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = lane <= i + e ? m[(i + e) * kLd + lane] : 0.f;
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                put(i + e, lane, v[e]);
+                put(i + e, 32 + lane, 0.f);
+            }
+        }
+    meet();                                            // T11's fp32 rows are read
+#pragma unroll 1
+    for (int i = r0; i < r0 + 16; i += 4) {
+        float z[4], v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            z[e] = -dot_row<8>(m + (i + e) * kLd + 32, x);
+            v[e] = lane <= i + e - 32 ? m[(i + e) * kLd + 32 + lane] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            put(i + e, lane, z[e]);
+            put(i + e, 32 + lane, v[e]);
+        }
+    }
+    tc::fence_proxy_async();
+    meet();
 }
 
 template <int NK>
-__global__ void __launch_bounds__(128) delta_prep_kernel(const PrepArgs p) {
+__global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, const __grid_constant__ CUtensorMap tm_q,
+                                                               const __grid_constant__ CUtensorMap tm_k) {
     if (p.err && *p.err != 0) return;
     extern __shared__ uint8_t raw[];
-    PrepSmem &sm = *reinterpret_cast<PrepSmem *>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
+    PrepSmem &sm = *reinterpret_cast<PrepSmem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const Block b = find_block(p.cu, p.nseqs, p.seqlen, p.nblk, blockIdx.x);
     if (b.nt == 0) return;
     const int h0 = blockIdx.y * p.heads_per_cta, R = p.H / p.G, grp = h0 / R;
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const __nv_bfloat16 *k = p.k + b.row * p.k_bs + b.t0 * p.k_ts + (int64_t)grp * p.N;
-#pragma unroll
-    for (int i = tid; i < kQ * NK / 8; i += 128) {
-        const int r = i / (NK / 8), c = i % (NK / 8) * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < b.nt && c < p.N) v = *reinterpret_cast<const uint4 *>(k + r * p.k_ts + c);
-        *reinterpret_cast<uint4 *>(sm.k + (c >> 6) * kTile + swz(r, c & 63)) = v;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    if (w == 0) tc::tmem_alloc(&sm.tmem, 64);
+    if (tid == 0) {
+        tc::mbar_init(&sm.mb, 1);
+        tc::mbar_init_fence();
+        sm.abort = 0;
     }
+    tc::fence_before_sync();
     __syncthreads();
-    float kk[8][4];
+    tc::fence_after_sync();
+    const uint32_t tm = sm.tmem;
+    bool ok = true;
+    if (tid == 0) {
+        // rows behind the sequence's end may hold anything: a product only meets its own two rows
+        tc::mbar_expect_tx(&sm.mb, NK / 64 * 2 * kTile);
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+        for (int x = 0; x < NK / 64; ++x) {
+            tma_load_4d(sm.kq + x * 2 * kTile, &tm_k, 64 * x, grp, (int)b.t0, (int)b.row, &sm.mb);
+            tma_load_4d(sm.kq + x * 2 * kTile + kTile, &tm_q, 64 * x, grp, (int)b.t0, (int)b.row, &sm.mb);
+        }
+        ok = wait_bar(&sm.mb, &sm.abort, 0, p.err);
+        tc::fence_after_sync();
+        const uint64_t d = tc::desc_sw128(tc::smem_u32(sm.kq), 16, 1024);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) kk[n][e] = 0.f;
-    const uint32_t kb = tc::smem_u32(sm.k);
-#pragma unroll
-    for (int s = 0; s < NK / 16; ++s) {
-        uint32_t a[4];
-        const uint32_t at = kb + (s >> 2) * kTile;
-        ldsm4(a, at + swz(16 * w + (lane & 15), (s & 3) * 16 + (lane >> 4) * 8));
-#pragma unroll
-        for (int n2 = 0; n2 < 4; ++n2)
-            if (n2 <= w) {
-                uint32_t bb[4];
-                ldsm4(bb, at + swz(16 * n2 + (lane & 7) + (lane >> 4) * 8, (s & 3) * 16 + ((lane >> 3) & 1) * 8));
-                mma16816(kk[2 * n2], a, bb[0], bb[1]);
-                mma16816(kk[2 * n2 + 1], a, bb[2], bb[3]);
-            }
+        for (int kk = 0; kk < NK / 16; ++kk) {
+            const uint32_t o = ((kk >> 2) * 2 * kTile + (kk & 3) * 32) >> 4;
+            tc::mma_bf16(tm, d + o, d + o, tc::idesc_bf16(128, 64, 0, 0), kk > 0);
+        }
+        tc::mma_commit(&sm.mb);
     }
-    for (int hh = 0; hh < p.heads_per_cta; ++hh) {
-        const int h = h0 + hh;
-        if (w == 0) {
+    __syncwarp();
+    ok = wait_bar(&sm.mb, &sm.abort, 1, p.err) && ok;
+    tc::fence_after_sync();
+    const uint32_t tl = tm + ((uint32_t)(32 * w) << 16);
+    const int i = (w & 1) * 32 + lane;                 // this thread's row of K K^T (warps 0, 1) or Q K^T (2, 3)
+    for (int hb = 0; hb < p.heads_per_cta; hb += kPair) {
+        const int nh = min(kPair, p.heads_per_cta - hb);
+        if (w >= 2 && w - 2 < nh) {
+            Gates &gt = sm.gates[w - 2];
+            const int h = h0 + hb + w - 2;
             const float *gp = p.g + b.row * p.g_bs + b.t0 * p.g_ts + h, *bp = p.beta + b.row * p.b_bs + b.t0 * p.b_ts + h;
             const float g0 = lane < b.nt ? fmaxf(gp[lane * p.g_ts], kMinLogDecay) : 0.f;
             const float g1 = lane + 32 < b.nt ? fmaxf(gp[(lane + 32) * p.g_ts], kMinLogDecay) : 0.f;
+            const float b0 = lane < b.nt ? bp[lane * p.b_ts] : 0.f, b1 = lane + 32 < b.nt ? bp[(lane + 32) * p.b_ts] : 0.f;
             double c0, c1, last;
             block_cs(g0, g1, c0, c1, last);
-            sm.hi[lane] = (float)c0;
-            sm.lo[lane] = (float)(c0 - (double)(float)c0);
-            sm.hi[lane + 32] = (float)c1;
-            sm.lo[lane + 32] = (float)(c1 - (double)(float)c1);
-            sm.beta[lane] = lane < b.nt ? bp[lane * p.b_ts] : 0.f;
-            sm.beta[lane + 32] = lane + 32 < b.nt ? bp[(lane + 32) * p.b_ts] : 0.f;
+            gt.hi[lane] = (float)c0;
+            gt.lo[lane] = (float)(c0 - (double)(float)c0);
+            gt.hi[lane + 32] = (float)c1;
+            gt.lo[lane + 32] = (float)(c1 - (double)(float)c1);
+            gt.beta[lane] = b0;
+            gt.beta[lane + 32] = b1;
         }
-        __syncthreads();
+        if (!__syncthreads_and(ok)) break;             // (the error word is set; nothing was computed)
+        for (int hh = 0; hh < nh; ++hh) {
+            const Gates &gt = sm.gates[hh];
+            const float ch = gt.hi[i], cl = gt.lo[i];
+            uint8_t *out = p.out + ((int64_t)blockIdx.x * p.H + h0 + hb + hh) * kHeadBytes;
+            if (w < 2) {
+                const float be = i < b.nt ? gt.beta[i] : 0.f;
+                float *row = sm.head[hh].m + i * kLd;
+#pragma unroll 1
+                for (int c = 0; c <= w; ++c) {         // (columns 32-63 of rows 0-31 are not read)
+                    float v[32];
+                    tc::tmem_ld32(tl + 32 * c, v);
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
-            if (n < 2 * (w + 1)) {
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 jh = *reinterpret_cast<const float4 *>(gt.hi + 32 * c + e);
+                        const float4 jl = *reinterpret_cast<const float4 *>(gt.lo + 32 * c + e);
+                        const float dh[4] = {jh.x, jh.y, jh.z, jh.w}, dl[4] = {jl.x, jl.y, jl.z, jl.w};
+                        float o[4];
 #pragma unroll
-                for (int e2 = 0; e2 < 2; ++e2) {
-                    const int i = 16 * w + g + 8 * e2, j = 8 * n + 2 * t;
-                    float2 v = make_float2(0.f, 0.f);
-                    if (j < i && i < b.nt)
-                        v.x = sm.beta[i] * ex2(((sm.hi[i] - sm.hi[j]) + (sm.lo[i] - sm.lo[j])) * kLog2e) * kk[n][2 * e2];
-                    if (j + 1 < i && i < b.nt)
-                        v.y = sm.beta[i] * ex2(((sm.hi[i] - sm.hi[j + 1]) + (sm.lo[i] - sm.lo[j + 1])) * kLog2e) *
-                              kk[n][2 * e2 + 1];
-                    *reinterpret_cast<float2 *>(sm.m + i * kLd + j) = v;
-                }
-            }
-        __syncthreads();
-        {   // column `lane % 16` of the inverse of diagonal block w
-            const int c = lane & 15;
-            float x[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float s = i == c ? 1.f : 0.f;
-                const float *row = sm.m + (16 * w + i) * kLd + 16 * w;
-#pragma unroll
-                for (int j4 = 0; j4 < i; j4 += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(row + j4);
-                    s = fmaf(-v.x, x[j4], s);
-                    if (j4 + 1 < i) s = fmaf(-v.y, x[j4 + 1], s);
-                    if (j4 + 2 < i) s = fmaf(-v.z, x[j4 + 2], s);
-                    if (j4 + 3 < i) s = fmaf(-v.w, x[j4 + 3], s);
-                }
-                x[i] = s;
-            }
-            if (lane < 16)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) sm.t[(16 * w + i) * kLd + 16 * w + c] = x[i];
-        }
-        __syncthreads();
-        {   // the blocks below it: tT[d] = transpose of T block (w + d, w)
-            float tT[3][2][4];
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    tT[0][s][e] = sm.t[(16 * w + 8 * s + 2 * t + (e & 1)) * kLd + 16 * w + g + 8 * (e >> 1)];
-#pragma unroll
-            for (int d = 1; d < 4; ++d) {
-                const int i = w + d;
-                if (i > 3) break;
-                float acc[2][4] = {}, out[2][4] = {};
-#pragma unroll
-                for (int dk = 0; dk < d; ++dk) mul16(acc, tT[dk], sm.m + 16 * i * kLd + 16 * (w + dk), g, t);
-                mul16(out, acc, sm.t + 16 * i * kLd + 16 * i, g, t);
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float v = -out[s][e];
-                        if (d < 3) tT[d][s][e] = v;
-                        sm.t[(16 * i + 8 * s + 2 * t + (e & 1)) * kLd + 16 * w + g + 8 * (e >> 1)] = v;
+                        for (int f = 0; f < 4; ++f)
+                            o[f] = 32 * c + e + f < i && i < b.nt
+                                       ? be * ex2(((ch - dh[f]) + (cl - dl[f])) * kLog2e) * v[e + f] : 0.f;
+                        *reinterpret_cast<float4 *>(row + 32 * c + e) = make_float4(o[0], o[1], o[2], o[3]);
                     }
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    float v[32];
+                    if (c <= w - 2) tc::tmem_ld32(tl + 32 * c, v);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t o[4] = {0, 0, 0, 0};
+                        if (c <= w - 2)
+#pragma unroll
+                            for (int f = 0; f < 4; ++f) {
+                                const int j = 32 * c + e + 2 * f;
+                                const float2 cj = *reinterpret_cast<const float2 *>(gt.hi + j);
+                                const float v0 = j <= i ? ex2((ch - cj.x) * kLog2e) * (v[e + 2 * f] * p.scale) : 0.f;
+                                const float v1 = j < i ? ex2((ch - cj.y) * kLog2e) * (v[e + 2 * f + 1] * p.scale) : 0.f;
+                                o[f] = pack2(v0, v1);
+                            }
+                        *reinterpret_cast<uint4 *>(out + kTBytes + swz(i, 32 * c + e)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+            }
+        }
+        __syncthreads();                               // M is written
+        if ((w & 1) < nh) {
+            Head &hd = sm.head[w & 1];
+            invert(hd, lane, w >> 1, 2 + (w & 1));
+            if (tid < 64 && lane == 0) {
+                uint8_t *out = p.out + ((int64_t)blockIdx.x * p.H + h0 + hb + w) * kHeadBytes;
+                bulk_store(out, hd.m, kTile);
+                bulk_store(out + kTile, hd.lo, kTile);
+                asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+                tc::bulk_wait_read();                  // the tile may be overwritten, or the CTA end
             }
         }
         __syncthreads();
-        uint8_t *out = p.T + ((int64_t)blockIdx.x * p.H + h) * kTBytes;
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            const int i = (tid >> 3) + 16 * it, c = (tid & 7) * 8;
-            uint32_t hi[4] = {}, lo[4] = {};
-            if (c <= (i | 15))
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 v = *reinterpret_cast<const float2 *>(sm.t + i * kLd + c + 2 * e);
-                    split2(v.x, v.y, hi[e], lo[e]);
-                }
-            *reinterpret_cast<uint4 *>(out + swz(i, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(out + kTile + swz(i, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (w == 0) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tm, 64);
     }
 }
 
 }  // namespace
 
-size_t delta_prep_bytes(const ssm_delta_args &a) { return (size_t)delta_slots(a) * a.nheads * kTBytes; }
+size_t delta_prep_bytes(const ssm_delta_args &a) { return (size_t)delta_slots(a) * a.nheads * dtc::kHeadBytes; }
 
-cudaError_t launch_delta_prep(const ssm_delta_args &a, const SeqView &sv, void *T, cudaStream_t st) {
+cudaError_t launch_delta_prep(const ssm_delta_args &a, const SeqView &sv, const CUtensorMap &tm_q,
+                              const CUtensorMap &tm_k, void *out, cudaStream_t st) {
     PrepArgs p;
-    p.k = static_cast<const __nv_bfloat16 *>(a.k);
-    p.k_bs = a.k_batch_stride; p.k_ts = a.k_token_stride;
     p.g = a.g; p.beta = a.beta;
     p.g_bs = a.g_batch_stride; p.g_ts = a.g_token_stride;
     p.b_bs = a.beta_batch_stride; p.b_ts = a.beta_token_stride;
     p.cu = a.cu_seqlens; p.err = sv.err; p.nseqs = sv.nseqs;
-    p.H = (int)a.nheads; p.G = (int)a.ngroups; p.N = (int)a.dstate;
+    p.H = (int)a.nheads; p.G = (int)a.ngroups;
     p.seqlen = a.seqlen; p.nblk = delta_blocks_per_row(a);
-    p.T = static_cast<uint8_t *>(T);
-    // as many heads of a group per CTA (they share K K^T) as leave the GPU full
+    p.scale = a.scale;
+    p.out = static_cast<uint8_t *>(out);
+    // as many heads of a group per CTA (they share [K; Q] K^T) as leave the GPU full
     const int64_t slots = delta_slots(a), R = a.nheads / a.ngroups;
     int hpc = (int)R;
-    while (hpc > 1 && (R % hpc != 0 || slots * (a.nheads / hpc) < 8LL * sm_count())) --hpc;
+    while (hpc > 1 && (R % hpc != 0 || slots * (a.nheads / hpc) < 16LL * sm_count())) --hpc;
     p.heads_per_cta = hpc;
     const dim3 grid((unsigned)slots, (unsigned)(a.nheads / hpc));
-    const size_t smem = sizeof(PrepSmem) + 128;
+    const size_t smem = sizeof(PrepSmem) + 1024;
     auto kernel = a.dstate <= 64 ? delta_prep_kernel<64> : delta_prep_kernel<128>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, 128, smem, st>>>(p);
+    kernel<<<grid, 128, smem, st>>>(p, tm_q, tm_k);
     return cudaGetLastError();
 }
 

@@ -12,11 +12,13 @@ namespace dtc {
 constexpr int kQ = 64;                    // tokens per block
 constexpr uint32_t kTile = 8192;          // 64 rows x 64 bf16: one 128-byte-swizzled tile
 constexpr size_t kTBytes = 2 * kTile;     // T of one (block, head): high and low parts
+constexpr size_t kHeadBytes = 3 * kTile;  // ... and its attention weights
 
 // Wait for an mbarrier phase, at most two seconds; gives up as soon as another
 // thread of the CTA has (`abort`), and records the timeout in the error word.
-SSM_DEVINL bool wait_bar(uint64_t *mb, volatile int *abort, uint32_t parity, int32_t *err) {
-    if (tc::mbar_try_wait(mb, parity)) return true;
+// The loop is kept out of line: a kernel of many roles waits in dozens of
+// places, and its loops have to stay within the instruction cache.
+static __device__ __noinline__ bool wait_slow(uint64_t *mb, volatile int *abort, uint32_t parity, int32_t *err) {
     const uint64_t t0 = tc::globaltimer_ns();
     for (;;) {
         if (*abort) return false;
@@ -26,6 +28,21 @@ SSM_DEVINL bool wait_bar(uint64_t *mb, volatile int *abort, uint32_t parity, int
     *abort = 1;
     if (err) atomicExch(err, SSM_DEVERR_TIMEOUT);
     return false;
+}
+SSM_DEVINL bool wait_bar(uint64_t *mb, volatile int *abort, uint32_t parity, int32_t *err) {
+    return tc::mbar_try_wait(mb, parity) || wait_slow(mb, abort, parity, err);
+}
+// Barrier 1 over `threads` threads that also tells whether `ok` holds in all of
+// them: warps that meet at a barrier give up together.
+template <int threads>
+SSM_DEVINL bool bar_all(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.and.pred q, 1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)ok), "n"(threads)
+        : "memory");
+    return r != 0;
 }
 SSM_DEVINL void arrive(uint64_t *mbar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_u32(mbar)) : "memory");
@@ -55,6 +72,53 @@ SSM_DEVINL void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+SSM_DEVINL void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// A load in two steps, so that other loads may stand between them; the values
+// pass through the wait, which keeps their uses behind it.
+SSM_DEVINL void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+SSM_DEVINL void tmem_ld32_wait(uint32_t (&r)[32], float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+    asm volatile(""
+                 : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31]));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+SSM_DEVINL void tmem_st16f(uint32_t taddr, const float (&v)[16]) {
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+    tmem_st16(taddr, r);
+}
+SSM_DEVINL void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 SSM_DEVINL void tmem_st32(uint32_t taddr, const float (&v)[32]) {
     uint32_t r[16];
 #pragma unroll
@@ -75,6 +139,14 @@ SSM_DEVINL uint32_t pack2(float a, float b) {
 SSM_DEVINL void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
     hi = pack2(a, b);
     lo = pack2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+}
+// 16 floats as operand columns: 8 columns of high parts at hi, of low parts at lo.
+SSM_DEVINL void st_split16(uint32_t hi, uint32_t lo, const float *v) {
+    uint32_t h[8], l[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
+    tmem_st8(hi, h);
+    tmem_st8(lo, l);
 }
 SSM_DEVINL void split32(const float (&v)[32], uint32_t (&hi)[16], uint32_t (&lo)[16]) {
 #pragma unroll

@@ -1,7 +1,8 @@
 // delta_tc_fwd.cu -- the gated delta rule in blocks of 64 tokens on the tensor
 // cores (bf16 activations, dstate <= 128).
 //
-// Per block, with the state h entering it and T from delta_prep.cu,
+// Per block, with the state h entering it and T and the attention weights from
+// delta_prep.cu,
 //     R_i = beta_i (v_i - exp(cs_i) h k_i),     U = T R,
 //     y_i = scale (exp(cs_i) h q_i + sum_{j<=i} exp(cs_i - cs_j) (q_i . k_j) u_j),
 //     h  <- exp(cs_last) h + sum_j exp(cs_last - cs_j) u_j k_j^T.
@@ -19,9 +20,15 @@
 // to bf16 once, like y itself.
 //
 // Roles: 8 warps for the chain (two per lane quarter, half of the columns
-// each), 4 for the output, one thread each for the chain's MMAs, the output's
-// MMAs and the loads (whose warp also computes the gate tables).  A block
-// costs three dependent MMA groups; the output's work fills the gaps.
+// each), 4 for the output, one thread for the MMAs and one warp for the loads
+// and the gate tables.  A block costs three
+// dependent groups of MMAs (h k with h q beside it, T R, the state's update)
+// with a pass over registers between them; each pass hands over its first half
+// as soon as it is written, so that the MMAs of that half overlap the second.
+// An MMA of 128 rows takes about 65 cycles whether it has 64 columns or
+// 128, so products that share the A operand are joined: K and Q lie one behind
+// the other and make one operand of 128 rows, and so do the two T of a CTA
+// whose halves are different heads.
 #include <string.h>
 
 #include "delta_tc.cuh"
@@ -29,32 +36,39 @@
 namespace ssm {
 
 size_t delta_prep_bytes(const ssm_delta_args &a);
-cudaError_t launch_delta_prep(const ssm_delta_args &a, const SeqView &sv, void *T, cudaStream_t st);
+cudaError_t launch_delta_prep(const ssm_delta_args &a, const SeqView &sv, const CUtensorMap &tm_q,
+                              const CUtensorMap &tm_k, void *out, cudaStream_t st);
 
 namespace {
 
 using namespace dtc;
 
+// A warp reaches the tensor-memory lanes of its number modulo 4.
 constexpr int kChainWarps = 8, kOutWarps = 4;
-constexpr int kThreads = (kChainWarps + kOutWarps + 3) * 32;
+constexpr int kOut0 = kChainWarps, kMmaWarp = kOut0 + kOutWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kThreads = (kLoadWarp + 1) * 32;
+static_assert(kOut0 % 4 == 0, "lane quarters");
 // tensor-memory columns
 constexpr uint32_t TM_H = 0;       // fp32 state, decayed for the next block
-constexpr uint32_t TM_HOP = 128;   // its two bf16 parts (64 columns each)
-constexpr uint32_t TM_RU = 256;    // h k, then U
-constexpr uint32_t TM_OP = 320;    // R, then the decayed u: two parts of 32 columns
-constexpr uint32_t TM_UOP = 384;   // u, high part
-constexpr uint32_t TM_O = 416;     // q k, h q, attention x u in turn
+constexpr uint32_t TM_HOP = 128;   // its two bf16 parts: per half of the pass 32 high, 32 low columns
+constexpr uint32_t TM_RU = 256;    // h k, then U (two heads: in 128 columns), then u as an operand (high part)
+constexpr uint32_t TM_HQ = 320;    // h q
+constexpr uint32_t TM_O = 384;     // scale exp(cs) h q, to which attention x u is added
+constexpr uint32_t TM_OP = 448;    // R, then the decayed u: two parts of 32 columns
 constexpr uint32_t kTmemCols = 512;
 
 enum Bar {
     B_FULL0, B_FULL1, B_EMPTY0, B_EMPTY1, B_TAB0, B_TAB1,
-    B_H, B_M1, B_R, B_M2, B_U, B_M3,           // the chain
-    B_QK, B_PM, B_M4, B_QHREAD, B_M5, B_OREAD, // the output
-    B_DRAIN, B_DRAIN2, B_COUNT
+    B_H0, B_H1, B_M1, B_R0, B_R1, B_M2, B_U0, B_U1, B_UOP, B_M3,    // the chain (halves 0 and 1 of a pass)
+    B_HQ, B_M5,                                                     // the output
+    B_DRAIN, B_COUNT
 };
 
+// Operand columns of the state's part (0 high, 1 low): states 32 b .. 32 b + 31 of column half cf.
+SSM_DEVINL uint32_t hop(int cf, int b, int part) { return TM_HOP + 64 * b + 32 * part + 16 * cf; }
+
 struct alignas(16) Tab {           // gates of one half of the rows, one block (read as float4)
-    float beta[kQ], bg[kQ], w[kQ], gs[kQ], cs[kQ];
+    float beta[kQ], bg[kQ], w[kQ], gs[kQ];
     float total;                   // exp(cs_last)
 };
 
@@ -66,10 +80,11 @@ struct Aux {
 };
 
 template <int NK, bool DUAL> struct Lay {
-    static constexpr uint32_t kKB = NK / 64 * kTile;
-    static constexpr uint32_t K = 0, Q = kKB, V = 2 * kKB, T = V + 2 * kTile;
-    static constexpr uint32_t stage = T + (DUAL ? 2 : 1) * (uint32_t)kTBytes;
-    static constexpr uint32_t PM = 2 * stage, AUX = PM + (DUAL ? 2 : 1) * kTile;
+    static constexpr uint32_t kKB = NK / 64 * 2 * kTile;             // per K-atom: 64 rows of K, 64 rows of Q
+    static constexpr uint32_t K = 0, V = kKB, T = V + 2 * kTile;      // T: high parts of both heads, low parts
+    static constexpr uint32_t kTPart = (DUAL ? 2 : 1) * kTile;
+    static constexpr uint32_t PM = T + 2 * kTPart, stage = PM + kTPart;
+    static constexpr uint32_t Y = 2 * stage, AUX = Y + 2 * kTile;
     static constexpr size_t bytes = AUX + sizeof(Aux) + 1024;
     static constexpr uint32_t tx = stage;
 };
@@ -77,7 +92,7 @@ template <int NK, bool DUAL> struct Lay {
 struct Args {
     ssm_delta_args a;
     SeqView sv;
-    const uint8_t *T;
+    const uint8_t *prep;           // delta_prep.cu: [slot][H][kHeadBytes]
     int64_t nblk;
     int R, nsl, units;             // heads per group, 64-row slices per head, CTAs per group
 };
@@ -132,10 +147,12 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
     const int64_t slot0 = seq_slot(a.cu_seqlens, s, p.nblk);
     if (warp == 0) tc::tmem_alloc(&ax.tmem, kTmemCols);
     if (tid == 0) {
+        constexpr int kEmpty = 1 + kChainWarps + kOutWarps;
         constexpr int counts[B_COUNT] = {
-            1, 1, 2 + kChainWarps + kOutWarps, 2 + kChainWarps + kOutWarps, 1, 1,
-            kChainWarps, 1, kChainWarps, 1, kChainWarps, 1,
-            1, kOutWarps, 1, kOutWarps, 1, kOutWarps, 1, 1};
+            1, 1, kEmpty, kEmpty, 1, 1,
+            kChainWarps, kChainWarps, 1, kChainWarps, kChainWarps, 1, kChainWarps, kChainWarps, kChainWarps, 1,
+            kOutWarps, 1,
+            1};
         for (int i = 0; i < B_COUNT; ++i) tc::mbar_init(&ax.mb[i], counts[i]);
         tc::mbar_init_fence();
         ax.abort = 0;
@@ -164,305 +181,294 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
         };
         bool ok = wait(B_TAB0, 0);
         // the entering state: NK / 2 columns of this thread's row
+#pragma unroll 1
+        for (int e = 0; e < NK / 32; ++e) {
+            const int c0 = cf * (NK / 2) + e * 16;
+            float v[16];
 #pragma unroll
-        for (int b = 0; b < NK / 64; ++b) {
-            const int c0 = cf * (NK / 2) + b * 32;
-            float v[32];
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
+            for (int i = 0; i < 16; i += 4) {
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (live && a.h0 && c0 + i < N) x = *reinterpret_cast<const float4 *>(a.h0 + srow + c0 + i);
                 v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
             }
-            uint32_t hi_[16], lo_[16];
-            split32(v, hi_, lo_);
-            tmem_st16(tl + TM_HOP + c0 / 2, hi_);
-            tmem_st16(tl + TM_HOP + 64 + c0 / 2, lo_);
+            st_split16(tl + hop(cf, e >> 1, 0) + 8 * (e & 1), tl + hop(cf, e >> 1, 1) + 8 * (e & 1), v);
             const float d = ax.tab[0][half].total;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= d;
-            tmem_st32(tl + TM_H + c0, v);
+            for (int i = 0; i < 16; ++i) v[i] *= d;
+            tmem_st16f(tl + TM_H + c0, v);
         }
-        arrive_st(B_H);
+        arrive_st(B_H0);
+        if (lane == 0) arrive(&ax.mb[B_H1]);
         for (int c = 0; c < n && ok; ++c) {
             const uint32_t ph = c & 1;
             const int stg = c & 1, nt = (int)min((int64_t)kQ, hi - lo - (int64_t)c * kQ);
             uint8_t *st = sm + stg * L::stage;
             const Tab &tb = ax.tab[stg][half];
-            // R = beta (v - exp(cs) h k)
-            ok = wait(B_FULL0 + stg, (c >> 1) & 1) && wait(B_TAB0 + stg, (c >> 1) & 1) && wait(B_M1, ph);
+            // R = beta (v - exp(cs) h k); what does not need h while the product runs
+            ok = wait(B_FULL0 + stg, (c >> 1) & 1) && wait(B_TAB0 + stg, (c >> 1) & 1);
             if (!ok) break;
-            tc::fence_after_sync();
+            const int t0 = cf * 32;
             float x[32];
-            uint32_t hi_[16], lo_[16];
-            tc::tmem_ld32(tl + TM_RU + cf * 32, x);
+            uint32_t raw_[32];
             {
+                float bv[32], bg[32];
                 const __nv_bfloat16 *v =
-                    reinterpret_cast<const __nv_bfloat16 *>(st + L::V + half * kTile) + (q & 1) * 32 + lane;
+                    reinterpret_cast<const __nv_bfloat16 *>(st + L::V + half * kTile) + t0 * 64 + (q & 1) * 32 + lane;
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
-                    const int t = cf * 32 + i;
-                    const float4 be = *reinterpret_cast<const float4 *>(tb.beta + t);
-                    const float4 bg = *reinterpret_cast<const float4 *>(tb.bg + t);
-                    const float bb[4] = {be.x, be.y, be.z, be.w}, gg[4] = {bg.x, bg.y, bg.z, bg.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float vv = __bfloat162float(v[(t + e) * 64]);
-                        x[i + e] = t + e < nt ? fmaf(-gg[e], x[i + e], bb[e] * vv) : 0.f;
+                    const float4 be = *reinterpret_cast<const float4 *>(tb.beta + t0 + i);
+                    const float4 g4 = *reinterpret_cast<const float4 *>(tb.bg + t0 + i);
+                    bv[i] = be.x * __bfloat162float(v[i * 64]);
+                    bv[i + 1] = be.y * __bfloat162float(v[(i + 1) * 64]);
+                    bv[i + 2] = be.z * __bfloat162float(v[(i + 2) * 64]);
+                    bv[i + 3] = be.w * __bfloat162float(v[(i + 3) * 64]);
+                    bg[i] = g4.x; bg[i + 1] = g4.y; bg[i + 2] = g4.z; bg[i + 3] = g4.w;
+                }
+                ok = wait(B_M1, ph);
+                if (!ok) break;
+                tc::fence_after_sync();
+                // all of h k is read before the first half of R lets U overwrite it
+                tmem_ld32_start(tl + TM_RU + t0, raw_);
+                if (nt < kQ) {                 // the keys behind the sequence's end may be anything
+                    for (int i = tid; i < (kQ - nt) * (NK / 8); i += kChainWarps * 32) {
+                        const int rr = nt + i / (NK / 8), cc = i % (NK / 8) * 8;
+                        *reinterpret_cast<uint4 *>(st + L::K + (cc >> 6) * 2 * kTile + swz(rr, cc & 63)) =
+                            make_uint4(0, 0, 0, 0);
                     }
+                    tc::fence_proxy_async();
                 }
+                tmem_ld32_wait(raw_, x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = fmaf(-bg[i], x[i], bv[i]);
             }
-            if (nt < kQ) {                     // the keys behind the sequence's end may be anything
-                for (int i = tid; i < (kQ - nt) * (NK / 8); i += kChainWarps * 32) {
-                    const int rr = nt + i / (NK / 8), cc = i % (NK / 8) * 8;
-                    *reinterpret_cast<uint4 *>(st + L::K + (cc >> 6) * kTile + swz(rr, cc & 63)) = make_uint4(0, 0, 0, 0);
-                }
-                tc::fence_proxy_async();
+            if (nt < kQ)                       // v and h k of the rows behind the end may be anything
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (t0 + i >= nt) x[i] = 0.f;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                st_split16(tl + TM_OP + t0 / 2 + 8 * b, tl + TM_OP + 32 + t0 / 2 + 8 * b, x + 16 * b);
+                arrive_st(B_R0 + b);
             }
-            split32(x, hi_, lo_);
-            tmem_st16(tl + TM_OP + cf * 16, hi_);
-            tmem_st16(tl + TM_OP + 32 + cf * 16, lo_);
-            arrive_st(B_R);
             // u = T R
-            ok = wait(B_M2, ph) && (c == 0 || wait(B_M5, ph ^ 1));
-            if (!ok) break;
-            tc::fence_after_sync();
-            tc::tmem_ld32(tl + TM_RU + cf * 32, x);
+            {
+                float w[32];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) hi_[i] = pack2(x[2 * i], x[2 * i + 1]);
-            tmem_st16(tl + TM_UOP + cf * 16, hi_);
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 w4 = *reinterpret_cast<const float4 *>(tb.w + t0 + i);
+                    w[i] = w4.x; w[i + 1] = w4.y; w[i + 2] = w4.z; w[i + 3] = w4.w;
+                }
+                ok = wait(B_M2, ph);
+                if (!ok) break;
+                tc::fence_after_sync();
+                tmem_ld32_start(tl + TM_RU + (DUAL && half ? 64 : 0) + t0, raw_);
+                tmem_ld32_wait(raw_, x);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 w = *reinterpret_cast<const float4 *>(tb.w + cf * 32 + i);
-                x[i] *= w.x; x[i + 1] *= w.y; x[i + 2] *= w.z; x[i + 3] *= w.w;
+                for (int b = 0; b < 2; ++b) {
+                    float y[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) y[i] = w[16 * b + i] * x[16 * b + i];
+                    st_split16(tl + TM_OP + t0 / 2 + 8 * b, tl + TM_OP + 32 + t0 / 2 + 8 * b, y);
+                    arrive_st(B_U0 + b);
+                }
             }
-            split32(x, hi_, lo_);
-            tmem_st16(tl + TM_OP + cf * 16, hi_);
-            tmem_st16(tl + TM_OP + 32 + cf * 16, lo_);
-            arrive_st(B_U);
+            // u for the output, over the 32 columns of U that this warp has read
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t h[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[i] = pack2(x[16 * b + 2 * i], x[16 * b + 2 * i + 1]);
+                tmem_st8(tl + TM_RU + t0 + 8 * b, h);
+            }
+            arrive_st(B_UOP);
             if (lane == 0) arrive(&ax.mb[B_EMPTY0 + stg]);
             // h
             const bool last = c + 1 == n;
-            ok = wait(B_M3, ph) && wait(B_M4, ph) && (last || wait(B_TAB0 + (stg ^ 1), ((c + 1) >> 1) & 1));
+            ok = last || wait(B_TAB0 + (stg ^ 1), ((c + 1) >> 1) & 1);
+            if (!ok) break;
+            const float d = last ? 1.f : ax.tab[stg ^ 1][half].total;
+            ok = wait(B_M3, ph);
             if (!ok) break;
             tc::fence_after_sync();
+            float h1[32];
+            uint32_t raw1[32];
+            tmem_ld32_start(tl + TM_H + cf * (NK / 2), raw_);
+            if (NK == 128) tmem_ld32_start(tl + TM_H + cf * (NK / 2) + 32, raw1);
+            tmem_ld32_wait(raw_, x);
+            if (NK == 128) tmem_ld32_wait(raw1, h1);
+            if (last) {
+                if (a.h_final && live)
+#pragma unroll
+                    for (int b = 0; b < NK / 64; ++b)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const int c0 = cf * (NK / 2) + b * 32 + i;
+                            const float *f = (b ? h1 : x) + i;
+                            if (c0 < N)
+                                *reinterpret_cast<float4 *>(a.h_final + srow + c0) = make_float4(f[0], f[1], f[2], f[3]);
+                        }
+                break;
+            }
 #pragma unroll
             for (int b = 0; b < NK / 64; ++b) {
-                const int c0 = cf * (NK / 2) + b * 32;
-                tc::tmem_ld32(tl + TM_H + c0, x);
-                if (last) {
-                    if (a.h_final && live)
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            if (c0 + i < N)
-                                *reinterpret_cast<float4 *>(a.h_final + srow + c0 + i) =
-                                    make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                } else {
-                    split32(x, hi_, lo_);
-                    tmem_st16(tl + TM_HOP + c0 / 2, hi_);
-                    tmem_st16(tl + TM_HOP + 64 + c0 / 2, lo_);
-                    const float d = ax.tab[stg ^ 1][half].total;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] *= d;
-                    tmem_st32(tl + TM_H + c0, x);
-                }
+                for (int e = 0; e < 2; ++e)
+                    st_split16(tl + hop(cf, b, 0) + 8 * e, tl + hop(cf, b, 1) + 8 * e, (b ? h1 : x) + 16 * e);
+                arrive_st(B_H0 + b);
             }
-            if (!last) arrive_st(B_H);
+            if (NK == 64 && lane == 0) arrive(&ax.mb[B_H1]);
+            // decayed for the next block's update; R, handed over later, covers these stores
+#pragma unroll
+            for (int b = 0; b < NK / 64; ++b) {
+                float *f = b ? h1 : x;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[i] *= d;
+                tmem_st32(tl + TM_H + cf * (NK / 2) + b * 32, b ? h1 : x);
+            }
         }
-    } else if (warp < kChainWarps + kOutWarps) {
+    } else if (warp < kMmaWarp) {
         // --------------------------------------------------------------- the output
-        const int q = warp - kChainWarps, half = q >> 1, r = row0[half] + (q & 1) * 32 + lane;
-        const bool live = half < halves && r < P;
+        const int q = warp - kOut0, half = q >> 1;
         const uint32_t tl = tm + ((uint32_t)(32 * q) << 16);
+        const int ch = (32 * q + lane) & 15, yh = ch >> 3;
+        const bool in = yh < halves && row0[yh] + (ch & 7) * 8 < P;
         __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + brow * a.y_batch_stride + lo * a.y_token_stride +
-                           (int64_t)head[half] * P + r;
-        auto arrive_w = [&](int b) {
-            __syncwarp();
-            if (lane == 0) arrive(&ax.mb[b]);
-        };
+                           (int64_t)head[yh] * P + row0[yh] + (ch & 7) * 8;
+        __nv_bfloat16 *ys = reinterpret_cast<__nv_bfloat16 *>(sm + L::Y);
         for (int c = 0; c < n; ++c) {
             const uint32_t ph = c & 1;
             const int stg = c & 1, nt = (int)min((int64_t)kQ, hi - lo - (int64_t)c * kQ);
-            // attention weights: rows i = 16 q + lane / 4 (+ 8), columns j
-            if (!wait(B_TAB0 + stg, (c >> 1) & 1) || !wait(B_QK, ph)) break;
+            float x[32];
+            // scale exp(cs) h q into the accumulator of attention x u
+            bool ok = wait(B_TAB0 + stg, (c >> 1) & 1) && wait(B_M1, ph);
             tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 1
             for (int b = 0; b < 2; ++b) {
-                uint32_t qk[16];
-                tc::tmem_ld16x256b_x4(tl + TM_O + 32 * b, qk);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int hh = 0; hh < (DUAL ? 2 : 1); ++hh) {
-                    const float *cs = ax.tab[stg][hh].cs;
-                    uint8_t *pm = sm + L::PM + hh * kTile;
-#pragma unroll
-                    for (int e2 = 0; e2 < 2; ++e2) {
-                        const int i = 16 * q + (lane >> 2) + 8 * e2;
-                        const float ci = cs[i];
-#pragma unroll
-                        for (int k8 = 0; k8 < 4; ++k8) {
-                            const int j = 32 * b + 8 * k8 + 2 * (lane & 3);
-                            const float2 cj = *reinterpret_cast<const float2 *>(cs + j);
-                            const float v0 = j <= i && i < nt ? a.scale * ex2(ci - cj.x) * __uint_as_float(qk[4 * k8 + 2 * e2]) : 0.f;
-                            const float v1 =
-                                j + 1 <= i && i < nt ? a.scale * ex2(ci - cj.y) * __uint_as_float(qk[4 * k8 + 2 * e2 + 1]) : 0.f;
-                            *reinterpret_cast<uint32_t *>(pm + swz(i, j)) = pack2(v0, v1);
-                        }
-                    }
-                }
-            }
-            tc::fence_proxy_async();
-            tc::fence_before_sync();
-            arrive_w(B_PM);
-            // scale exp(cs) h q
-            if (!wait(B_M4, ph)) break;
-            tc::fence_after_sync();
-            float o[64], x[32];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                tc::tmem_ld32(tl + TM_O + 32 * b, x);
+                tc::tmem_ld32(tl + TM_HQ + 32 * b, x);
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
                     const float4 gs = *reinterpret_cast<const float4 *>(ax.tab[stg][half].gs + 32 * b + i);
-                    o[32 * b + i] = x[i] * gs.x;
-                    o[32 * b + i + 1] = x[i + 1] * gs.y;
-                    o[32 * b + i + 2] = x[i + 2] * gs.z;
-                    o[32 * b + i + 3] = x[i + 3] * gs.w;
+                    x[i] *= gs.x; x[i + 1] *= gs.y; x[i + 2] *= gs.z; x[i + 3] *= gs.w;
                 }
+                tmem_st32(tl + TM_O + 32 * b, x);
             }
+            tmem_wait_st();
             tc::fence_before_sync();
-            arrive_w(B_QHREAD);
-            if (lane == 0) arrive(&ax.mb[B_EMPTY0 + stg]);
-            if (!wait(B_M5, ph)) break;
+            __syncwarp();
+            if (lane == 0) {
+                arrive(&ax.mb[B_HQ]);
+                arrive(&ax.mb[B_EMPTY0 + stg]);
+            }
+            ok = ok && wait(B_M5, ph);
             tc::fence_after_sync();
-#pragma unroll
+            // y by way of shared memory: whole 16-byte pieces of token rows
+#pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 tc::tmem_ld32(tl + TM_O + 32 * b, x);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[32 * b + i] += x[i];
+                for (int i = 0; i < 32; ++i) ys[(32 * b + i) * 128 + 32 * q + lane] = __float2bfloat16_rn(x[i]);
             }
-            tc::fence_before_sync();
-            arrive_w(B_OREAD);
-            if (live) {
+            if (!bar_all<128>(ok)) break;
+            if (in) {
                 __nv_bfloat16 *yc = y + (int64_t)c * kQ * a.y_token_stride;
 #pragma unroll
-                for (int i = 0; i < kQ; ++i)
-                    if (i < nt) yc[i * a.y_token_stride] = __float2bfloat16_rn(o[i]);
-            }
-        }
-    } else if (warp == kChainWarps + kOutWarps) {
-        // ----------------------------------------------------- MMAs of the chain
-        constexpr uint32_t ID1 = tc::idesc_bf16(128, 64, 0, 0), ID3 = tc::idesc_bf16(128, NK, 0, 1);
-        for (int c = 0; c < n; ++c) {
-            const uint32_t ph = c & 1;
-            const int stg = c & 1;
-            const uint32_t st = sb + stg * L::stage;
-            const uint64_t dK = tc::desc_sw128(st + L::K, 16, 1024), dKm = tc::desc_sw128(st + L::K, kTile, 1024);
-            if (!wait(B_FULL0 + stg, (c >> 1) & 1) || !wait(B_H, ph)) break;
-            tc::fence_after_sync();
-            if (lane == 0) {
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int kk = 0; kk < NK / 16; ++kk)
-                        mma_ts(tm + TM_RU, tm + TM_HOP + part * 64 + kk * 8,
-                               dK + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4), ID1, part + kk > 0);
-                tc::mma_commit(&ax.mb[B_M1]);
-            }
-            __syncwarp();
-            if (!wait(B_R, ph)) break;
-            tc::fence_after_sync();
-            if (lane == 0) {
-                // U = T R: (R high, T low), (R low, T high), (R high, T high)
-#pragma unroll
-                for (int hh = 0; hh < (DUAL ? 2 : 1); ++hh) {
-                    const uint64_t dT = tc::desc_sw128(st + L::T + hh * (uint32_t)kTBytes, 16, 1024);
-#pragma unroll
-                    for (int part = 0; part < 3; ++part)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            const uint32_t A = tm + TM_OP + (part == 1 ? 32 : 0) + kk * 8;
-                            const uint64_t B = dT + (part == 0 ? kTile >> 4 : 0) + kk * 2;
-                            if constexpr (DUAL)
-                                mma_ts_lanes(tm + TM_RU, A, B, ID1, part + kk > 0, hh ? ~0u : 0u, hh ? 0u : ~0u);
-                            else
-                                mma_ts(tm + TM_RU, A, B, ID1, part + kk > 0);
-                        }
+                for (int i = 0; i < 8; ++i) {
+                    const int t = 2 * q + (lane >> 4) + 8 * i;
+                    if (t < nt)
+                        *reinterpret_cast<uint4 *>(yc + t * a.y_token_stride) =
+                            *reinterpret_cast<const uint4 *>(ys + t * 128 + ch * 8);
                 }
-                tc::mma_commit(&ax.mb[B_M2]);
             }
-            __syncwarp();
-            if (!wait(B_U, ph)) break;
-            tc::fence_after_sync();
-            if (lane == 0) {
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(tm + TM_H, tm + TM_OP + part * 32 + kk * 8, dKm + kk * 128, ID3, 1);
-                tc::mma_commit(&ax.mb[B_M3]);
-                tc::mma_commit(&ax.mb[B_EMPTY0 + stg]);
-            }
-            __syncwarp();
+            asm volatile("bar.sync 1, 128;\n" ::: "memory");
         }
-    } else if (warp == kChainWarps + kOutWarps + 1) {
-        // ---------------------------------------------------- MMAs of the output
-        constexpr uint32_t ID1 = tc::idesc_bf16(128, 64, 0, 0), IDQ = tc::idesc_bf16(64, 64, 0, 0);
-        auto qk = [&](int c) {
-            const uint32_t st = sb + (c & 1) * L::stage;
-            const uint64_t dQ = tc::desc_sw128(st + L::Q, 16, 1024), dK = tc::desc_sw128(st + L::K, 16, 1024);
-            if (!wait(B_FULL0 + (c & 1), (c >> 1) & 1)) return false;
-            tc::fence_after_sync();
-            if (lane == 0) {
-#pragma unroll
-                for (int kk = 0; kk < NK / 16; ++kk) {
-                    const uint32_t o = ((kk >> 2) * kTile + (kk & 3) * 32) >> 4;
-                    tc::mma_bf16(tm + TM_O, dQ + o, dK + o, IDQ, kk > 0);
-                }
-                tc::mma_commit(&ax.mb[B_QK]);
-            }
-            __syncwarp();
-            return true;
-        };
-        bool ok = qk(0);
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------------ MMAs
+        constexpr uint32_t ID1 = tc::idesc_bf16(128, 128, 0, 0), ID2 = tc::idesc_bf16(128, DUAL ? 128 : 64, 0, 0),
+                           ID3 = tc::idesc_bf16(128, NK, 0, 1), ID5 = tc::idesc_bf16(128, 64, 0, 0);
+        bool ok = true;
         for (int c = 0; c < n && ok; ++c) {
             const uint32_t ph = c & 1;
             const int stg = c & 1;
-            const uint64_t dQ = tc::desc_sw128(sb + stg * L::stage + L::Q, 16, 1024);
-            ok = wait(B_H, ph) && wait(B_PM, ph);
+            const uint32_t st = sb + stg * L::stage;
+            const uint64_t dK = tc::desc_sw128(st + L::K, 16, 1024), dKm = tc::desc_sw128(st + L::K, 2 * kTile, 1024);
+            const uint64_t dT = tc::desc_sw128(st + L::T, 16, 1024), dP = tc::desc_sw128(st + L::PM, 16, 1024);
+            // h k and h q, once the last block's output has read h q and used u
+            ok = wait(B_FULL0 + stg, (c >> 1) & 1) &&
+                 (c == 0 || (wait(B_HQ, ph ^ 1) && wait(B_M5, ph ^ 1)));
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                ok = ok && wait(B_H0 + b, ph);
+                if (!ok) break;
+                tc::fence_after_sync();
+                if (lane == 0) {
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int k4 = 0; k4 < NK / 32; ++k4) {
+                            // the first half of a pass: states 32 cf ... of each column half
+                            const int kk = NK == 64 ? 2 * b + k4 : (k4 >> 1) * 4 + 2 * b + (k4 & 1);
+                            mma_ts(tm + TM_RU, tm + hop(NK == 64 ? b : k4 >> 1, NK == 64 ? 0 : b, part) + (k4 & 1) * 8,
+                                   dK + (((kk >> 2) * 2 * kTile + (kk & 3) * 32) >> 4), ID1, b + part + k4 > 0);
+                        }
+                    if (b) tc::mma_commit(&ax.mb[B_M1]);
+                }
+                __syncwarp();
+            }
+            // U = T R: (R high, T low), (R low, T high), (R high, T high)
+            ok = ok && (!DUAL || wait(B_HQ, ph));
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                ok = ok && wait(B_R0 + b, ph);
+                if (!ok) break;
+                tc::fence_after_sync();
+                if (lane == 0) {
+#pragma unroll
+                    for (int part = 0; part < 3; ++part)
+#pragma unroll
+                        for (int k2 = 0, kk = b; k2 < 2; ++k2, kk += 2)
+                            mma_ts(tm + TM_RU, tm + TM_OP + (part == 1 ? 32 : 0) + kk * 8,
+                                   dT + (part == 0 ? L::kTPart >> 4 : 0) + kk * 2, ID2, b + part + kk > 0);
+                    if (b) tc::mma_commit(&ax.mb[B_M2]);
+                }
+                __syncwarp();
+            }
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                ok = ok && wait(B_U0 + b, ph);
+                if (!ok) break;
+                tc::fence_after_sync();
+                if (lane == 0) {
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int k2 = 0, kk = b; k2 < 2; ++k2, kk += 2)
+                            mma_ts(tm + TM_H, tm + TM_OP + part * 32 + kk * 8, dKm + kk * 128, ID3, 1);
+                    if (b) {
+                        tc::mma_commit(&ax.mb[B_M3]);
+                    }
+                }
+                __syncwarp();
+            }
+            // attention x u
+            ok = ok && wait(B_UOP, ph) && wait(B_HQ, ph);
             if (!ok) break;
             tc::fence_after_sync();
             if (lane == 0) {
 #pragma unroll
-                for (int kk = 0; kk < NK / 16; ++kk)
-                    mma_ts(tm + TM_O, tm + TM_HOP + kk * 8, dQ + (((kk >> 2) * kTile + (kk & 3) * 32) >> 4), ID1, kk > 0);
-                tc::mma_commit(&ax.mb[B_M4]);
+                for (int hh = 0; hh < (DUAL ? 2 : 1); ++hh)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t A = tm + TM_RU + (kk >> 1) * 32 + (kk & 1) * 8;
+                        const uint64_t B = dP + hh * (kTile >> 4) + kk * 2;
+                        if constexpr (DUAL)
+                            mma_ts_lanes(tm + TM_O, A, B, ID5, 1, hh ? ~0u : 0u, hh ? 0u : ~0u);
+                        else
+                            mma_ts(tm + TM_O, A, B, ID5, 1);
+                    }
+                tc::mma_commit(&ax.mb[B_M5]);
                 tc::mma_commit(&ax.mb[B_EMPTY0 + stg]);
             }
             __syncwarp();
-            ok = wait(B_QHREAD, ph) && wait(B_U, ph);
-            if (!ok) break;
-            tc::fence_after_sync();
-            if (lane == 0) {
-#pragma unroll
-                for (int hh = 0; hh < (DUAL ? 2 : 1); ++hh) {
-                    const uint64_t dP = tc::desc_sw128(sb + L::PM + hh * kTile, 16, 1024);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        if constexpr (DUAL)
-                            mma_ts_lanes(tm + TM_O, tm + TM_UOP + kk * 8, dP + kk * 2, ID1, kk > 0, hh ? ~0u : 0u,
-                                         hh ? 0u : ~0u);
-                        else
-                            mma_ts(tm + TM_O, tm + TM_UOP + kk * 8, dP + kk * 2, ID1, kk > 0);
-                }
-                tc::mma_commit(&ax.mb[B_M5]);
-            }
-            __syncwarp();
-            ok = wait(B_OREAD, ph);
-            if (ok && c + 1 < n) {
-                tc::fence_after_sync();
-                ok = qk(c + 1);
-            }
         }
     } else {
         // --------------------------------------------------- loads and gate tables
@@ -488,16 +494,18 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
                 tc::mbar_expect_tx(mb, L::tx);
 #pragma unroll
                 for (int x = 0; x < NK / 64; ++x) {
-                    tma_load_4d(st + L::K + x * kTile, &tm_k, 64 * x, grp, (int)t0, (int)brow, mb);
-                    tma_load_4d(st + L::Q + x * kTile, &tm_q, 64 * x, grp, (int)t0, (int)brow, mb);
+                    tma_load_4d(st + L::K + x * 2 * kTile, &tm_k, 64 * x, grp, (int)t0, (int)brow, mb);
+                    tma_load_4d(st + L::K + x * 2 * kTile + kTile, &tm_q, 64 * x, grp, (int)t0, (int)brow, mb);
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     tc::tma_load_3d(st + L::V + i * kTile, &tm_v, (int)(head[i] * P + row0[i]), (int)t0, (int)brow, mb);
 #pragma unroll
                 for (int i = 0; i < (DUAL ? 2 : 1); ++i)
-                    bulk_load(st + L::T + i * (uint32_t)kTBytes, p.T + ((slot0 + c) * H + head[i]) * kTBytes,
-                              (uint32_t)kTBytes, mb);
+#pragma unroll
+                    for (int part = 0; part < 3; ++part)       // T high, T low, attention weights
+                        bulk_load(st + L::T + part * L::kTPart + i * kTile,
+                                  p.prep + ((slot0 + c) * H + head[i]) * kHeadBytes + part * kTile, kTile, mb);
             }
             issued = c + 1;
 #pragma unroll
@@ -517,7 +525,6 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
                     tb.bg[t] = bv[hh][e] * ec;
                     tb.w[t] = exp_d(last - cs[e]);
                     tb.gs[t] = a.scale * ec;
-                    tb.cs[t] = (float)(cs[e] * 1.4426950408889634);
                 }
                 if (lane == 0) tb.total = exp_d(last);
             }
@@ -527,11 +534,10 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
         if (*ab && lane == 0)                  // copies in flight land before the CTA ends
             for (int c = max(0, issued - 2); c < issued; ++c) tc::mbar_wait(&ax.mb[B_FULL0 + (c & 1)], (c >> 1) & 1, 1u << 22);
     }
-    if (*ab && lane == 0 && (warp == kChainWarps + kOutWarps || warp == kChainWarps + kOutWarps + 1)) {
-        // after a wait that ran out: the MMAs this thread issued complete before tensor memory is freed
-        uint64_t *mb = &ax.mb[warp == kChainWarps + kOutWarps ? B_DRAIN : B_DRAIN2];
-        tc::mma_commit(mb);
-        tc::mbar_wait(mb, 0, 1u << 22);
+    if (*ab && lane == 0 && warp == kMmaWarp) {
+        // after a wait that ran out: the MMAs in flight complete before tensor memory is freed
+        tc::mma_commit(&ax.mb[B_DRAIN]);
+        tc::mbar_wait(&ax.mb[B_DRAIN], 0, 1u << 22);
     }
     __syncwarp();
     tc::fence_before_sync();
@@ -563,7 +569,7 @@ bool delta_tc_ok(const ssm_delta_args &a) {
     };
     return delta_tc_shape(a) && a.seqlen > 0 && al(a.q, a.q_batch_stride, a.q_token_stride) &&
            al(a.k, a.k_batch_stride, a.k_token_stride) && al(a.v, a.v_batch_stride, a.v_token_stride) &&
-           al(a.h0, 0, 0) && al(a.h_final, 0, 0);
+           al(a.y, a.y_batch_stride, a.y_token_stride) && al(a.h0, 0, 0) && al(a.h_final, 0, 0);
 }
 size_t delta_tc_workspace_bytes(const ssm_delta_args &a) { return delta_prep_bytes(a); }
 
@@ -573,7 +579,7 @@ cudaError_t launch_delta_tc(const ssm_delta_args &a, const SeqView &sv, void *ws
     Args p;
     p.a = a;
     p.sv = sv;
-    p.T = static_cast<const uint8_t *>(ws);
+    p.prep = static_cast<const uint8_t *>(ws);
     p.nblk = delta_blocks_per_row(a);
     p.R = (int)(a.nheads / a.ngroups);
     p.nsl = (int)((a.headdim + 63) / 64);
@@ -585,7 +591,7 @@ cudaError_t launch_delta_tc(const ssm_delta_args &a, const SeqView &sv, void *ws
         !make_map_box(&v, a.v, a.nheads * a.headdim, a.seqlen, rows,
                       a.seqlen > 1 ? a.v_token_stride : a.nheads * a.headdim, a.v_batch_stride, false, kQ))
         return cudaErrorInvalidValue;
-    cudaError_t e = launch_delta_prep(a, sv, ws, st);
+    cudaError_t e = launch_delta_prep(a, sv, q, k, ws, st);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.ngroups * p.units), (unsigned)nseq);
     const bool dual = p.nsl % 2 != 0;

@@ -7,8 +7,6 @@
 // a CTA own the groups next to each other of one token, so a CTA reads a
 // contiguous stretch.  A unit stays with its group, which keeps the weights
 // (forward) and their gradients' sums (backward) in registers over its tokens.
-// Mean and M2 = sum (x - mean)^2 are merged pairwise (Chan's update) in one
-// reduction: no cancellation however far the mean is from zero.
 //
 // Backward, with n the normalised values, t = n w + bias, dt = dL/dt, dn = dt w:
 //     ds = r (dn - n mean(dn n) - [subtract_mean] mean(dn)),  r = 1/sqrt(var + eps)
@@ -31,62 +29,28 @@ struct Args {
     int splits;              // units per group
 };
 
-// Sum of (n, mean, M2) triples over the unit's TPU threads; every thread gets
-// the result.  `red` holds 3 floats per warp of the CTA.
-SSM_DEVINL void merge(float &n, float &mean, float &m2, float nb, float mb, float m2b) {
-    const float nn = n + nb;
-    if (nn > 0.f) {
-        const float d = mb - mean, f = nb / nn;
-        m2 = m2 + m2b + d * d * n * f;
-        mean = fmaf(d, f, mean);
-    }
-    n = nn;
-}
-template <int TPU>
-SSM_DEVINL void unit_stats(float &n, float &mean, float &m2, float *red) {
-#pragma unroll
-    for (int o = 1; o < (TPU < 32 ? TPU : 32); o <<= 1) {
-        const float nb = __shfl_xor_sync(~0u, n, o), mb = __shfl_xor_sync(~0u, mean, o),
-                    m2b = __shfl_xor_sync(~0u, m2, o);
-        merge(n, mean, m2, nb, mb, m2b);
-    }
-    if constexpr (TPU > 32) {
-        const int warp = threadIdx.x >> 5, first = warp / (TPU / 32) * (TPU / 32);
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) {
-            red[3 * warp] = n;
-            red[3 * warp + 1] = mean;
-            red[3 * warp + 2] = m2;
-        }
-        __syncthreads();
-        n = red[3 * first];
-        mean = red[3 * first + 1];
-        m2 = red[3 * first + 2];
-#pragma unroll
-        for (int i = 1; i < TPU / 32; ++i)
-            merge(n, mean, m2, red[3 * (first + i)], red[3 * (first + i) + 1], red[3 * (first + i) + 2]);
-    }
-}
-template <int TPU>
-SSM_DEVINL void unit_sum2(float &u, float &v, float *red) {
+// Sum of u (and of v) over the unit's TPU threads; every thread gets it.
+// `red` holds 2 floats per warp of the CTA.
+template <int TPU, bool TWO>
+SSM_DEVINL void unit_sum(float &u, float &v, float *red) {
 #pragma unroll
     for (int o = 1; o < (TPU < 32 ? TPU : 32); o <<= 1) {
         u += __shfl_xor_sync(~0u, u, o);
-        v += __shfl_xor_sync(~0u, v, o);
+        if (TWO) v += __shfl_xor_sync(~0u, v, o);
     }
     if constexpr (TPU > 32) {
         const int warp = threadIdx.x >> 5, first = warp / (TPU / 32) * (TPU / 32);
         __syncthreads();
         if ((threadIdx.x & 31) == 0) {
             red[2 * warp] = u;
-            red[2 * warp + 1] = v;
+            if (TWO) red[2 * warp + 1] = v;
         }
         __syncthreads();
         u = v = 0.f;
 #pragma unroll
         for (int i = 0; i < TPU / 32; ++i) {
             u += red[2 * (first + i)];
-            v += red[2 * (first + i) + 1];
+            if (TWO) v += red[2 * (first + i) + 1];
         }
     }
 }
@@ -97,87 +61,121 @@ template <int TPU, bool VEC>
 SSM_DEVINL int chan(int th, int i, int e) {
     return VEC ? (i * TPU + th) * 8 + e : (i * 8 + e) * TPU + th;
 }
+// Whether the group holds it (VEC: groups are whole runs, so e does not matter).
+template <int TPU, bool VEC>
+SSM_DEVINL bool held(int th, int i, int e, int D) { return chan<TPU, VEC>(th, i, VEC ? 0 : e) < D; }
+
+// 8 VPT values of this thread as they lie in memory: bf16 stays packed until it
+// is used, which halves the registers that loads in flight occupy.
+template <typename T, int VPT> struct Raw;
+template <int VPT> struct Raw<float, VPT> {
+    float v[VPT][8];
+    SSM_DEVINL float get(int i, int e) const { return v[i][e]; }
+};
+template <int VPT> struct Raw<__nv_bfloat16, VPT> {
+    uint32_t w[VPT][4];
+    SSM_DEVINL float get(int i, int e) const {
+        return __uint_as_float(e & 1 ? w[i][e >> 1] & 0xffff0000u : w[i][e >> 1] << 16);
+    }
+};
 template <typename T, int TPU, int VPT, bool VEC>
-SSM_DEVINL void load(float (&v)[VPT][8], const T *p, int th, int D) {
+SSM_DEVINL void load(Raw<T, VPT> &r, const T *p, int th, int D) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        if constexpr (VEC) {
-            if (chan<TPU, VEC>(th, i, 0) < D) Vec8<T>::ld(p + chan<TPU, VEC>(th, i, 0), v[i]);
+        if constexpr (VEC && sizeof(T) == 2) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (held<TPU, VEC>(th, i, 0, D)) x = *reinterpret_cast<const uint4 *>(p + chan<TPU, VEC>(th, i, 0));
+            r.w[i][0] = x.x; r.w[i][1] = x.y; r.w[i][2] = x.z; r.w[i][3] = x.w;
+        } else if constexpr (VEC) {
+            if (held<TPU, VEC>(th, i, 0, D)) Vec8<float>::ld(p + chan<TPU, VEC>(th, i, 0), r.v[i]);
             else
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+                for (int e = 0; e < 8; ++e) r.v[i][e] = 0.f;
+        } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const int c0 = chan<TPU, VEC>(th, i, e), c1 = chan<TPU, VEC>(th, i, e + 1);
+                const uint32_t x = c0 < D ? __bfloat16_as_ushort(p[c0]) : 0, y = c1 < D ? __bfloat16_as_ushort(p[c1]) : 0;
+                r.w[i][e >> 1] = x | y << 16;
+            }
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = chan<TPU, VEC>(th, i, e);
-                v[i][e] = c < D ? Elem<T>::ld(p + c) : 0.f;
+                r.v[i][e] = c < D ? p[c] : 0.f;
             }
         }
     }
 }
 template <typename T, int TPU, int VPT, bool VEC>
-SSM_DEVINL void store(T *p, const float (&v)[VPT][8], int th, int D) {
+SSM_DEVINL void store(T *p, const float (&v)[8], int th, int i, int D) {
+    if constexpr (VEC) {
+        if (held<TPU, VEC>(th, i, 0, D)) Vec8<T>::st(p + chan<TPU, VEC>(th, i, 0), v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        if constexpr (VEC) {
-            if (chan<TPU, VEC>(th, i, 0) < D) Vec8<T>::st(p + chan<TPU, VEC>(th, i, 0), v[i]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = chan<TPU, VEC>(th, i, e);
-                if (c < D) Elem<T>::st(p + c, v[i][e]);
-            }
+        for (int e = 0; e < 8; ++e) {
+            const int c = chan<TPU, VEC>(th, i, e);
+            if (c < D) Elem<T>::st(p + c, v[e]);
         }
     }
 }
 
-SSM_DEVINL float sigmoid(float v) { return 1.f / (1.f + __expf(-v)); }
+// 1 / (1 + e^-v) on the MUFU unit: two operations of 2^-22 relative error each;
+// for v << 0 the power overflows to infinity and its reciprocal is 0.
+SSM_DEVINL float sigmoid(float v) { return rcp(1.f + ex2(-v * kLog2e)); }
+
+// Batch and token of a row number (rows < 2^31): no division for one batch row.
+SSM_DEVINL void split_row(const ssm_norm_args &a, int64_t row, int64_t &b, int64_t &t) {
+    b = 0;
+    t = row;
+    if (a.batch > 1) {
+        const uint32_t n = (uint32_t)a.seqlen, q = (uint32_t)row / n;
+        b = q;
+        t = (uint32_t)row - q * n;
+    }
+}
 
 template <int TPU> constexpr int threads_of() { return TPU > 256 ? TPU : 256; }
+// What z does: nothing, gate the result, gate the input.
+enum Kind { kNoGate, kGate, kGateFirst };
 
-// mean and 1 / sqrt(var + eps) of the group this unit holds in v
-template <int TPU, int VPT, bool VEC>
-SSM_DEVINL void stats(const float (&v)[VPT][8], int th, int D, bool centre, float eps, float *red, float &mean, float &r) {
-    float n = 0.f, m2 = 0.f;
+// mean and 1 / sqrt(var + eps) of the group whose values this unit's threads
+// give (zeros past the group): the mean first, then the centred squares, which
+// loses no digits however far the mean is from zero.
+template <int TPU, int VPT, bool VEC, typename F>
+SSM_DEVINL void stats(F get, int th, int D, float inv, bool centre, float eps, float *red, float &mean, float &r) {
+    float m2 = 0.f, none = 0.f;
     mean = 0.f;
     if (centre) {
-        float s = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (chan<TPU, VEC>(th, i, e) < D) {
-                    s += v[i][e];
-                    n += 1.f;
-                }
-        mean = n > 0.f ? s / n : 0.f;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (chan<TPU, VEC>(th, i, e) < D) m2 = fmaf(v[i][e] - mean, v[i][e] - mean, m2);
-        unit_stats<TPU>(n, mean, m2, red);
-    } else {
-        float none = 0.f;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m2 = fmaf(v[i][e], v[i][e], m2);      // zeros past D
-        unit_sum2<TPU>(m2, none, red);
+            for (int e = 0; e < 8; ++e) mean += get(i, e);
+        unit_sum<TPU, false>(mean, none, red);
+        mean *= inv;
     }
-    r = 1.f / sqrtf(m2 / (float)D + eps);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float d = held<TPU, VEC>(th, i, e, D) ? get(i, e) - mean : 0.f;
+            m2 = fmaf(d, d, m2);
+        }
+    unit_sum<TPU, false>(m2, none, red);
+    r = rsqrtf(fmaf(m2, inv, eps));
 }
 
-template <typename T, int TPU, int VPT, bool VEC>
+template <typename T, int TPU, int VPT, bool VEC, Kind K>
 __global__ void __launch_bounds__(threads_of<TPU>()) group_norm_kernel(const Args p) {
-    __shared__ float red[threads_of<TPU>() / 32 * 3];
+    __shared__ float red[threads_of<TPU>() / 32 * 2];
     const ssm_norm_args &a = p.a;
     constexpr int UPB = threads_of<TPU>() / TPU;
     const int th = threadIdx.x % TPU, D = (int)(a.channels / a.groups);
+    const float inv = 1.f / (float)D;
     const int64_t unit = (int64_t)blockIdx.x * UPB + threadIdx.x / TPU;
     const int64_t grp = unit % a.groups, first = unit / a.groups;
     const int64_t c0 = grp * D;
-    const bool gated = a.mode == SSM_NORM_GATE, pre = a.mode == SSM_NORM_GATE_FIRST, act = a.mode == SSM_NORM_SILU;
+    const bool act = a.mode == SSM_NORM_SILU;
     float w[VPT][8], b[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -188,47 +186,66 @@ __global__ void __launch_bounds__(threads_of<TPU>()) group_norm_kernel(const Arg
             b[i][e] = a.bias && c < D ? a.bias[c0 + c] : 0.f;
         }
     // the same number of turns for every unit of a CTA: the sums of wide groups synchronise
-    const int64_t turns = (p.rows + p.splits - 1) / p.splits;
-    for (int64_t it = 0; it < turns; ++it) {
-        const int64_t row = first + it * p.splits;
+    const int turns = (int)((p.rows + p.splits - 1) / p.splits);
+    Raw<T, VPT> x, z;
+    const auto fetch = [&](int it, Raw<T, VPT> &x, Raw<T, VPT> &z) {
+        const int64_t row = first + (int64_t)it * p.splits;
         const bool live = first < p.splits && row < p.rows;
-        if (TPU <= 32 && __all_sync(~0u, !live)) break;
-        const int64_t bi = live ? row / a.seqlen : 0, t = live ? row % a.seqlen : 0;
-        float x[VPT][8], z[VPT][8];
+        int64_t bi, t;
+        split_row(a, live ? row : 0, bi, t);
         const int dl = live ? D : 0;
         load<T, TPU, VPT, VEC>(x, (const T *)a.x + bi * a.x_batch_stride + t * a.x_token_stride + c0, th, dl);
-        if (gated || pre) load<T, TPU, VPT, VEC>(z, (const T *)a.z + bi * a.z_batch_stride + t * a.z_token_stride + c0, th, dl);
-        if (pre)
+        if (K != kNoGate)
+            load<T, TPU, VPT, VEC>(z, (const T *)a.z + bi * a.z_batch_stride + t * a.z_token_stride + c0, th, dl);
+    };
+    fetch(0, x, z);
+    for (int it = 0; it < turns; ++it) {
+        const int64_t row = first + (int64_t)it * p.splits;
+        const bool live = first < p.splits && row < p.rows;
+        if (TPU <= 32 && __all_sync(~0u, !live)) break;
+        Raw<T, VPT> xn, zn;                            // the next token's values, in flight meanwhile
+        if (it + 1 < turns) fetch(it + 1, xn, zn);
+        float s[K == kGateFirst ? VPT : 1][8];
+        if (K == kGateFirst)
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[i][e] *= z[i][e] * sigmoid(z[i][e]);
+                for (int e = 0; e < 8; ++e) s[K == kGateFirst ? i : 0][e] = x.get(i, e) * z.get(i, e) * sigmoid(z.get(i, e));
+        const auto in = [&](int i, int e) { return K == kGateFirst ? s[K == kGateFirst ? i : 0][e] : x.get(i, e); };
         float mean, r;
-        stats<TPU, VPT, VEC>(x, th, D, a.subtract_mean != 0, a.eps, red, mean, r);
-        if (!live) continue;
+        stats<TPU, VPT, VEC>(in, th, D, inv, a.subtract_mean != 0, a.eps, red, mean, r);
+        if (live) {
+            int64_t bi, t;
+            split_row(a, row, bi, t);
+            T *y = (T *)a.y + bi * a.y_batch_stride + t * a.y_token_stride + c0;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
+            for (int i = 0; i < VPT; ++i) {
+                float o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float v = fmaf((x[i][e] - mean) * r, w[i][e], b[i][e]);
-                if (gated) v *= z[i][e] * sigmoid(z[i][e]);
-                if (act) v *= sigmoid(v);
-                x[i][e] = v;
+                for (int e = 0; e < 8; ++e) {
+                    float v = fmaf((in(i, e) - mean) * r, w[i][e], b[i][e]);
+                    if (K == kGate) v *= z.get(i, e) * sigmoid(z.get(i, e));
+                    if (K == kNoGate && act) v *= sigmoid(v);
+                    o[e] = v;
+                }
+                store<T, TPU, VPT, VEC>(y, o, th, i, D);
             }
-        store<T, TPU, VPT, VEC>((T *)a.y + bi * a.y_batch_stride + t * a.y_token_stride + c0, x, th, D);
+        }
+        x = xn;
+        z = zn;
     }
 }
 
-template <typename T, int TPU, int VPT, bool VEC>
+template <typename T, int TPU, int VPT, bool VEC, Kind K>
 __global__ void __launch_bounds__(threads_of<TPU>()) group_norm_bwd_kernel(const Args p) {
-    __shared__ float red[threads_of<TPU>() / 32 * 3];
+    __shared__ float red[threads_of<TPU>() / 32 * 2];
     const ssm_norm_args &a = p.a;
     constexpr int UPB = threads_of<TPU>() / TPU;
     const int th = threadIdx.x % TPU, D = (int)(a.channels / a.groups);
     const int64_t unit = (int64_t)blockIdx.x * UPB + threadIdx.x / TPU;
     const int64_t grp = unit % a.groups, first = unit / a.groups;
     const int64_t c0 = grp * D;
-    const bool gated = a.mode == SSM_NORM_GATE, pre = a.mode == SSM_NORM_GATE_FIRST, act = a.mode == SSM_NORM_SILU;
+    const bool act = a.mode == SSM_NORM_SILU;
     const float inv = 1.f / (float)D;
     float w[VPT][8], b[VPT][8], dw[VPT][8], db[VPT][8];
 #pragma unroll
@@ -237,73 +254,96 @@ __global__ void __launch_bounds__(threads_of<TPU>()) group_norm_bwd_kernel(const
         for (int e = 0; e < 8; ++e) {
             const int c = chan<TPU, VEC>(th, i, e);
             w[i][e] = a.weight && c < D ? a.weight[c0 + c] : 1.f;
-            b[i][e] = a.bias && c < D ? a.bias[c0 + c] : 0.f;
+            // the bias matters only where the gradient looks at t itself
+            b[i][e] = K != kGateFirst && a.bias && c < D ? a.bias[c0 + c] : 0.f;
             dw[i][e] = db[i][e] = 0.f;
         }
-    const int64_t turns = (p.rows + p.splits - 1) / p.splits;
-    for (int64_t it = 0; it < turns; ++it) {
-        const int64_t row = first + it * p.splits;
+    const int turns = (int)((p.rows + p.splits - 1) / p.splits);
+    Raw<T, VPT> x, z, g;
+    const auto fetch = [&](int it, Raw<T, VPT> &x, Raw<T, VPT> &z, Raw<T, VPT> &g) {
+        const int64_t row = first + (int64_t)it * p.splits;
         const bool live = first < p.splits && row < p.rows;
-        if (TPU <= 32 && __all_sync(~0u, !live)) break;
-        const int64_t bi = live ? row / a.seqlen : 0, t = live ? row % a.seqlen : 0;
+        int64_t bi, t;
+        split_row(a, live ? row : 0, bi, t);
         const int dl = live ? D : 0;
-        float x[VPT][8], z[VPT][8], g[VPT][8], s[VPT][8];
         load<T, TPU, VPT, VEC>(x, (const T *)a.x + bi * a.x_batch_stride + t * a.x_token_stride + c0, th, dl);
         load<T, TPU, VPT, VEC>(g, (const T *)p.dy + bi * p.dy_bs + t * p.dy_ts + c0, th, dl);
-        if (gated || pre) load<T, TPU, VPT, VEC>(z, (const T *)a.z + bi * a.z_batch_stride + t * a.z_token_stride + c0, th, dl);
+        if (K != kNoGate)
+            load<T, TPU, VPT, VEC>(z, (const T *)a.z + bi * a.z_batch_stride + t * a.z_token_stride + c0, th, dl);
+    };
+    fetch(0, x, z, g);
+    for (int it = 0; it < turns; ++it) {
+        const int64_t row = first + (int64_t)it * p.splits;
+        const bool live = first < p.splits && row < p.rows;
+        if (TPU <= 32 && __all_sync(~0u, !live)) break;
+        Raw<T, VPT> xn, zn, gn;
+        // with one vector per thread there are registers for the next token's loads
+        if (VPT == 1 && it + 1 < turns) fetch(it + 1, xn, zn, gn);
+        float s[VPT][8], sg[K == kNoGate ? 1 : VPT][8], dn[VPT][8];
+        float dz[K == kGate ? VPT : 1][8];
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[i][e] = pre ? x[i][e] * z[i][e] * sigmoid(z[i][e]) : x[i][e];
+            for (int e = 0; e < 8; ++e) {
+                if (K != kNoGate) sg[K == kNoGate ? 0 : i][e] = sigmoid(z.get(i, e));
+                s[i][e] = K == kGateFirst ? x.get(i, e) * (z.get(i, e) * sg[K == kNoGate ? 0 : i][e]) : x.get(i, e);
+            }
         float mean, r;
-        stats<TPU, VPT, VEC>(s, th, D, a.subtract_mean != 0, a.eps, red, mean, r);
+        stats<TPU, VPT, VEC>([&](int i, int e) { return s[i][e]; }, th, D, inv, a.subtract_mean != 0, a.eps, red, mean, r);
+        if (!live) r = 0.f;                            // (eps = 0: 1 / sqrt(0) of no token must not meet dy = 0)
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const bool in = chan<TPU, VEC>(th, i, e) < dl;
-                const float n = in ? (s[i][e] - mean) * r : 0.f;
-                float dt = g[i][e];
-                if (gated || act) {
-                    const float tt = fmaf(n, w[i][e], b[i][e]);
-                    if (gated) {
-                        const float sg = sigmoid(z[i][e]);
-                        const float gate = z[i][e] * sg;
-                        z[i][e] = dt * tt * fmaf(gate, 1.f - sg, sg);          // dz
-                        dt *= gate;
-                    } else {
-                        const float sg = sigmoid(tt);
-                        dt *= fmaf(tt * sg, 1.f - sg, sg);
-                    }
+                // dy is 0 past the group and for a token that is not there, and with it all that is summed
+                const float n = (s[i][e] - mean) * r;
+                float dt = g.get(i, e);
+                if (K == kGate) {
+                    const float sv = sg[K == kNoGate ? 0 : i][e], gate = z.get(i, e) * sv;
+                    dz[K == kGate ? i : 0][e] = dt * fmaf(n, w[i][e], b[i][e]) * fmaf(gate, 1.f - sv, sv);
+                    dt *= gate;
+                } else if (K == kNoGate && act) {
+                    const float t = fmaf(n, w[i][e], b[i][e]), sv = sigmoid(t);
+                    dt *= fmaf(t * sv, 1.f - sv, sv);
                 }
                 s[i][e] = n;
                 dw[i][e] = fmaf(dt, n, dw[i][e]);
                 db[i][e] += dt;
-                g[i][e] = dt * w[i][e];                                         // dn
-                s1 += g[i][e];
-                s2 = fmaf(g[i][e], n, s2);
+                dn[i][e] = dt * w[i][e];
+                s1 += dn[i][e];
+                s2 = fmaf(dn[i][e], n, s2);
             }
-        unit_sum2<TPU>(s1, s2, red);
-        if (!live) continue;
-        s1 = a.subtract_mean ? s1 * inv : 0.f;
-        s2 *= inv;
+        unit_sum<TPU, true>(s1, s2, red);
+        if (live) {
+            s1 = a.subtract_mean ? s1 * inv : 0.f;
+            s2 *= inv;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
+            for (int i = 0; i < VPT; ++i) {
+                float o[8], o2[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float d = r * (g[i][e] - s1 - s[i][e] * s2);
-                if (pre) {
-                    const float sg = sigmoid(z[i][e]);
-                    const float gate = z[i][e] * sg;
-                    z[i][e] = d * x[i][e] * fmaf(gate, 1.f - sg, sg);          // dz
-                    x[i][e] = d * gate;
-                } else {
-                    x[i][e] = d;
+                for (int e = 0; e < 8; ++e) {
+                    const float d = r * (dn[i][e] - s1 - s[i][e] * s2);
+                    o[e] = d;
+                    if (K == kGateFirst) {
+                        const float sv = sg[K == kNoGate ? 0 : i][e], gate = z.get(i, e) * sv;
+                        o2[e] = d * x.get(i, e) * fmaf(gate, 1.f - sv, sv);
+                        o[e] = d * gate;
+                    } else if (K == kGate) {
+                        o2[e] = dz[K == kGate ? i : 0][e];
+                    }
                 }
+                store<T, TPU, VPT, VEC>((T *)p.dx + row * a.channels + c0, o, th, i, D);
+                if (K != kNoGate) store<T, TPU, VPT, VEC>((T *)p.dz + row * a.channels + c0, o2, th, i, D);
             }
-        store<T, TPU, VPT, VEC>((T *)p.dx + row * a.channels + c0, x, th, D);
-        if (gated || pre) store<T, TPU, VPT, VEC>((T *)p.dz + row * a.channels + c0, z, th, D);
+        }
+        if (VPT == 1) {
+            x = xn;
+            z = zn;
+            g = gn;
+        } else if (it + 1 < turns) {
+            fetch(it + 1, x, z, g);
+        }
     }
     if (p.pw && first < p.splits) {
 #pragma unroll
@@ -347,59 +387,68 @@ __global__ void __launch_bounds__(256) norm_shares_kernel(const float *pw, const
 }
 
 // Threads per unit and 8-channel vectors per thread for a group of D channels:
-// the narrowest unit that holds the group, so that few lanes idle.
+// the narrowest unit that holds the group, so that few lanes idle (fewer shapes
+// without 16-byte accesses, where the loads cost more than idle lanes).
 struct Shape {
     int tpu, vpt;
 };
-Shape shape_of(int64_t D) {
-    if (D <= 64) return {8, 1};
-    if (D <= 128) return {16, 1};
+Shape shape_of(int64_t D, bool vec) {
+    if (vec && D <= 64) return {8, 1};
+    if (vec && D <= 128) return {16, 1};
     if (D <= 256) return {32, 1};
-    if (D <= 512) return {32, 2};
+    if (vec && D <= 512) return {32, 2};
     if (D <= 1024) return {128, 1};
-    if (D <= 2048) return {128, 2};
+    if (vec && D <= 2048) return {128, 2};
     if (D <= 4096) return {256, 2};
     return {512, 4};
 }
 
-int splits_of(const ssm_norm_args &a, int ctas_per_sm) {
-    const Shape s = shape_of(a.channels / a.groups);
-    const int threads = s.tpu > 256 ? s.tpu : 256, upb = threads / s.tpu;
-    const int64_t rows = a.batch * a.seqlen;
-    const int64_t units = (int64_t)sm_count() * ctas_per_sm * upb;
+// Units per group: as many as fill the GPU at `warps` warps per SM, so that a
+// unit keeps its weights over many tokens.
+int splits_of(const ssm_norm_args &a, bool vec, int warps) {
+    const Shape s = shape_of(a.channels / a.groups, vec);
+    const int64_t rows = a.batch * a.seqlen, units = (int64_t)sm_count() * warps * 32 / s.tpu;
     int64_t n = units / a.groups;
     if (n < 1) n = 1;
     return (int)(n < rows ? n : rows);
 }
-// CTAs per SM: as many as the registers allow (two 512-thread CTAs at most).
-int fwd_ctas(const ssm_norm_args &a) { return shape_of(a.channels / a.groups).tpu > 256 ? 1 : 4; }
-int bwd_ctas(const ssm_norm_args &a) { return shape_of(a.channels / a.groups).tpu > 256 ? 1 : 2; }
+constexpr int kFwdWarps = 32, kBwdWarps = 16;
 
-template <bool BWD, typename T, int TPU, int VPT>
-void run(const Args &p, bool vec, cudaStream_t st) {
+template <bool BWD, typename T, int TPU, int VPT, bool VEC, Kind K>
+void run(const Args &p, cudaStream_t st) {
     constexpr int UPB = threads_of<TPU>() / TPU;
     const int64_t units = (int64_t)p.splits * p.a.groups;
     const unsigned grid = (unsigned)((units + UPB - 1) / UPB);
-    if constexpr (BWD) {
-        if (vec) group_norm_bwd_kernel<T, TPU, VPT, true><<<grid, threads_of<TPU>(), 0, st>>>(p);
-        else group_norm_bwd_kernel<T, TPU, VPT, false><<<grid, threads_of<TPU>(), 0, st>>>(p);
+    if constexpr (BWD) group_norm_bwd_kernel<T, TPU, VPT, VEC, K><<<grid, threads_of<TPU>(), 0, st>>>(p);
+    else group_norm_kernel<T, TPU, VPT, VEC, K><<<grid, threads_of<TPU>(), 0, st>>>(p);
+}
+template <bool BWD, typename T, Kind K>
+void pick(const Args &p, bool vec, cudaStream_t st) {
+    const Shape s = shape_of(p.a.channels / p.a.groups, vec);
+    if (vec) {
+        if (s.tpu == 8) run<BWD, T, 8, 1, true, K>(p, st);
+        else if (s.tpu == 16) run<BWD, T, 16, 1, true, K>(p, st);
+        else if (s.tpu == 32 && s.vpt == 1) run<BWD, T, 32, 1, true, K>(p, st);
+        else if (s.tpu == 32) run<BWD, T, 32, 2, true, K>(p, st);
+        else if (s.tpu == 128 && s.vpt == 1) run<BWD, T, 128, 1, true, K>(p, st);
+        else if (s.tpu == 128) run<BWD, T, 128, 2, true, K>(p, st);
+        else if (s.tpu == 256) run<BWD, T, 256, 2, true, K>(p, st);
+        else run<BWD, T, 512, 4, true, K>(p, st);
     } else {
-        if (vec) group_norm_kernel<T, TPU, VPT, true><<<grid, threads_of<TPU>(), 0, st>>>(p);
-        else group_norm_kernel<T, TPU, VPT, false><<<grid, threads_of<TPU>(), 0, st>>>(p);
+        if (s.tpu == 32) run<BWD, T, 32, 1, false, K>(p, st);
+        else if (s.tpu == 128) run<BWD, T, 128, 1, false, K>(p, st);
+        else if (s.tpu == 256) run<BWD, T, 256, 2, false, K>(p, st);
+        else run<BWD, T, 512, 4, false, K>(p, st);
     }
 }
-template <bool BWD, typename T>
-cudaError_t pick(const Args &p, bool vec, cudaStream_t st) {
-    const Shape s = shape_of(p.a.channels / p.a.groups);
+template <bool BWD>
+cudaError_t launch(const Args &p, bool vec, cudaStream_t st) {
+    const bool bf = p.a.dtype == SSM_BF16;
     timing_begin(st);
-    if (s.tpu == 8) run<BWD, T, 8, 1>(p, vec, st);
-    else if (s.tpu == 16) run<BWD, T, 16, 1>(p, vec, st);
-    else if (s.tpu == 32 && s.vpt == 1) run<BWD, T, 32, 1>(p, vec, st);
-    else if (s.tpu == 32) run<BWD, T, 32, 2>(p, vec, st);
-    else if (s.tpu == 128 && s.vpt == 1) run<BWD, T, 128, 1>(p, vec, st);
-    else if (s.tpu == 128) run<BWD, T, 128, 2>(p, vec, st);
-    else if (s.tpu == 256) run<BWD, T, 256, 2>(p, vec, st);
-    else run<BWD, T, 512, 4>(p, vec, st);
+    if (p.a.mode == SSM_NORM_GATE) bf ? pick<BWD, __nv_bfloat16, kGate>(p, vec, st) : pick<BWD, float, kGate>(p, vec, st);
+    else if (p.a.mode == SSM_NORM_GATE_FIRST)
+        bf ? pick<BWD, __nv_bfloat16, kGateFirst>(p, vec, st) : pick<BWD, float, kGateFirst>(p, vec, st);
+    else bf ? pick<BWD, __nv_bfloat16, kNoGate>(p, vec, st) : pick<BWD, float, kNoGate>(p, vec, st);
     timing_end(st);
     return cudaGetLastError();
 }
@@ -416,18 +465,20 @@ cudaError_t launch_group_norm(const ssm_norm_args &a, cudaStream_t st) {
     p.a = a;
     p.rows = a.batch * a.seqlen;
     if (p.rows == 0) return cudaSuccess;
-    p.splits = splits_of(a, fwd_ctas(a));
     const size_t es = a.dtype == SSM_BF16 ? 2 : 4;
     const bool vec = (a.channels / a.groups) % 8 == 0 && vec_ok(a.x, a.x_batch_stride, a.x_token_stride, es) &&
                      vec_ok(a.z, a.z_batch_stride, a.z_token_stride, es) &&
                      vec_ok(a.y, a.y_batch_stride, a.y_token_stride, es);
-    return a.dtype == SSM_BF16 ? pick<false, __nv_bfloat16>(p, vec, st) : pick<false, float>(p, vec, st);
+    p.splits = splits_of(a, vec, kFwdWarps);
+    return launch<false>(p, vec, st);
 }
 
 size_t group_norm_bwd_workspace_bytes(const ssm_norm_bwd_args &b) {
     const ssm_norm_args &a = b.fwd;
     if (a.batch * a.seqlen == 0) return 0;
-    return 2 * (((size_t)splits_of(a, bwd_ctas(a)) * a.channels * 4 + 255) / 256 * 256);
+    // shapes alone decide the size: room for the layout with more units per group
+    const int n = splits_of(a, true, kBwdWarps), m = splits_of(a, false, kBwdWarps);
+    return 2 * (((size_t)(n > m ? n : m) * a.channels * 4 + 255) / 256 * 256);
 }
 
 cudaError_t launch_group_norm_bwd(const ssm_norm_bwd_args &b, void *ws, cudaStream_t st) {
@@ -446,7 +497,6 @@ cudaError_t launch_group_norm_bwd(const ssm_norm_bwd_args &b, void *ws, cudaStre
         if (e == cudaSuccess && b.dbias) e = cudaMemsetAsync(b.dbias, 0, a.channels * 4, st);
         return e;
     }
-    p.splits = splits_of(a, bwd_ctas(a));
     if (b.dweight || b.dbias) {
         p.pw = static_cast<float *>(ws);
         p.pb = reinterpret_cast<float *>(static_cast<char *>(ws) + group_norm_bwd_workspace_bytes(b) / 2);
@@ -456,7 +506,8 @@ cudaError_t launch_group_norm_bwd(const ssm_norm_bwd_args &b, void *ws, cudaStre
                      vec_ok(a.z, a.z_batch_stride, a.z_token_stride, es) &&
                      vec_ok(b.dy, b.dy_batch_stride, b.dy_token_stride, es) && vec_ok(b.dx, 0, 0, es) &&
                      vec_ok(b.dz, 0, 0, es);
-    cudaError_t e = a.dtype == SSM_BF16 ? pick<true, __nv_bfloat16>(p, vec, st) : pick<true, float>(p, vec, st);
+    p.splits = splits_of(a, vec, kBwdWarps);
+    cudaError_t e = launch<true>(p, vec, st);
     if (e != cudaSuccess || !p.pw) return e;
     norm_shares_kernel<<<(unsigned)((a.channels + 31) / 32), 256, 0, st>>>(p.pw, p.pb, p.splits, a.channels, b.dweight,
                                                                           b.dbias);

@@ -91,7 +91,7 @@ ssm_status validate_norm(const ssm_norm_args *a, const void *y, int64_t y_bs, in
     const bool work = a->batch > 0 && a->seqlen > 0;
     if (work && gate != (a->z != nullptr)) return SSM_ERR_INVALID_ARG;
     if (a->channels / a->groups > ssm::kMaxGroupWidth || a->channels > INT32_MAX || a->seqlen > INT32_MAX ||
-        a->batch > INT32_MAX)
+        a->batch > INT32_MAX || a->batch * a->seqlen > INT32_MAX)
         return SSM_ERR_UNSUPPORTED;
     const size_t es = esize(a->dtype);
     SSM_TRY(check_act(a->x, a->x_batch_stride, a->x_token_stride, a->channels, a->batch, a->seqlen, es, work));
