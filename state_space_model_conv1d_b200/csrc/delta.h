@@ -28,6 +28,9 @@ bool delta_tc_shape(const ssm_delta_args &a);
 bool delta_tc_ok(const ssm_delta_args &a);
 size_t delta_tc_workspace_bytes(const ssm_delta_args &a);
 cudaError_t launch_delta_tc(const ssm_delta_args &a, const SeqView &sv, void *ws, cudaStream_t st);
+bool delta_tc_bwd_ok(const ssm_delta_bwd_args &b);
+size_t delta_tc_bwd_workspace_bytes(const ssm_delta_bwd_args &b);
+cudaError_t launch_delta_tc_bwd(const ssm_delta_bwd_args &b, const SeqView &sv, void *ws, cudaStream_t st);
 
 cudaError_t launch_delta_update(const ssm_delta_update_args &a, cudaStream_t st);
 

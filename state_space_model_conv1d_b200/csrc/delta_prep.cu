@@ -22,6 +22,7 @@
 #include <string.h>
 
 #include "delta_tc.cuh"
+#include "delta_tc.h"
 
 namespace ssm {
 namespace {
@@ -39,7 +40,8 @@ struct PrepArgs {
     int nseqs, H, G, heads_per_cta;
     int64_t seqlen, nblk;
     float scale;
-    uint8_t *out;                          // [slot][H][kHeadBytes]
+    uint8_t *out;                          // [slot][H][kHeadBytes or kHeadBytesBwd]
+    int bwd;
 };
 
 struct Gates {
@@ -232,6 +234,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
     ok = wait_bar(&sm.mb, &sm.abort, 1, p.err) && ok;
     tc::fence_after_sync();
     const uint32_t tl = tm + ((uint32_t)(32 * w) << 16);
+    const int64_t hbytes = p.bwd ? kHeadBytesBwd : kHeadBytes;
     const int i = (w & 1) * 32 + lane;                 // this thread's row of K K^T (warps 0, 1) or Q K^T (2, 3)
     for (int hb = 0; hb < p.heads_per_cta; hb += kPair) {
         const int nh = min(kPair, p.heads_per_cta - hb);
@@ -241,7 +244,11 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
             const float *gp = p.g + b.row * p.g_bs + b.t0 * p.g_ts + h, *bp = p.beta + b.row * p.b_bs + b.t0 * p.b_ts + h;
             const float g0 = lane < b.nt ? fmaxf(gp[lane * p.g_ts], kMinLogDecay) : 0.f;
             const float g1 = lane + 32 < b.nt ? fmaxf(gp[(lane + 32) * p.g_ts], kMinLogDecay) : 0.f;
-            const float b0 = lane < b.nt ? bp[lane * p.b_ts] : 0.f, b1 = lane + 32 < b.nt ? bp[(lane + 32) * p.b_ts] : 0.f;
+            float b0 = lane < b.nt ? bp[lane * p.b_ts] : 0.f, b1 = lane + 32 < b.nt ? bp[(lane + 32) * p.b_ts] : 0.f;
+            if (p.bwd) {
+                b0 = bwd_beta(b0);
+                b1 = bwd_beta(b1);
+            }
             double c0, c1, last;
             block_cs(g0, g1, c0, c1, last);
             gt.hi[lane] = (float)c0;
@@ -255,7 +262,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
         for (int hh = 0; hh < nh; ++hh) {
             const Gates &gt = sm.gates[hh];
             const float ch = gt.hi[i], cl = gt.lo[i];
-            uint8_t *out = p.out + ((int64_t)blockIdx.x * p.H + h0 + hb + hh) * kHeadBytes;
+            uint8_t *out = p.out + ((int64_t)blockIdx.x * p.H + h0 + hb + hh) * hbytes;
             if (w < 2) {
                 const float be = i < b.nt ? gt.beta[i] : 0.f;
                 float *row = sm.head[hh].m + i * kLd;
@@ -283,17 +290,22 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
                     if (c <= w - 2) tc::tmem_ld32(tl + 32 * c, v);
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
-                        uint32_t o[4] = {0, 0, 0, 0};
-                        if (c <= w - 2)
+                        uint32_t o[4] = {0, 0, 0, 0}, ol[4] = {0, 0, 0, 0};
+                        if (c <= w - 2 && i < b.nt)
 #pragma unroll
                             for (int f = 0; f < 4; ++f) {
                                 const int j = 32 * c + e + 2 * f;
                                 const float2 cj = *reinterpret_cast<const float2 *>(gt.hi + j);
-                                const float v0 = j <= i ? ex2((ch - cj.x) * kLog2e) * (v[e + 2 * f] * p.scale) : 0.f;
-                                const float v1 = j < i ? ex2((ch - cj.y) * kLog2e) * (v[e + 2 * f + 1] * p.scale) : 0.f;
-                                o[f] = pack2(v0, v1);
+                                const float2 lj = *reinterpret_cast<const float2 *>(gt.lo + j);
+                                const float e0 = ex2(((ch - cj.x) + (cl - lj.x)) * kLog2e);
+                                const float e1 = ex2(((ch - cj.y) + (cl - lj.y)) * kLog2e);
+                                const float v0 = j <= i ? e0 * (v[e + 2 * f] * p.scale) : 0.f;
+                                const float v1 = j < i ? e1 * (v[e + 2 * f + 1] * p.scale) : 0.f;
+                                split2(v0, v1, o[f], ol[f]);
                             }
-                        *reinterpret_cast<uint4 *>(out + kTBytes + swz(i, 32 * c + e)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        uint8_t *at = out + kTBytes + swz(i, 32 * c + e);
+                        *reinterpret_cast<uint4 *>(at) = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (p.bwd) *reinterpret_cast<uint4 *>(at + kTile) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
                     }
                 }
             }
@@ -303,7 +315,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
             Head &hd = sm.head[w & 1];
             invert(hd, lane, w >> 1, 2 + (w & 1));
             if (tid < 64 && lane == 0) {
-                uint8_t *out = p.out + ((int64_t)blockIdx.x * p.H + h0 + hb + w) * kHeadBytes;
+                uint8_t *out = p.out + ((int64_t)blockIdx.x * p.H + h0 + hb + w) * hbytes;
                 bulk_store(out, hd.m, kTile);
                 bulk_store(out + kTile, hd.lo, kTile);
                 asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
@@ -322,10 +334,12 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
 
 }  // namespace
 
-size_t delta_prep_bytes(const ssm_delta_args &a) { return (size_t)delta_slots(a) * a.nheads * dtc::kHeadBytes; }
+size_t delta_prep_bytes(const ssm_delta_args &a, bool bwd) {
+    return (size_t)delta_slots(a) * a.nheads * (bwd ? dtc::kHeadBytesBwd : dtc::kHeadBytes);
+}
 
-cudaError_t launch_delta_prep(const ssm_delta_args &a, const SeqView &sv, const CUtensorMap &tm_q,
-                              const CUtensorMap &tm_k, void *out, cudaStream_t st) {
+cudaError_t launch_delta_prep(const ssm_delta_args &a, const SeqView &sv, const DeltaMaps &m, void *out, bool bwd,
+                              cudaStream_t st) {
     PrepArgs p;
     p.g = a.g; p.beta = a.beta;
     p.g_bs = a.g_batch_stride; p.g_ts = a.g_token_stride;
@@ -335,6 +349,7 @@ cudaError_t launch_delta_prep(const ssm_delta_args &a, const SeqView &sv, const 
     p.seqlen = a.seqlen; p.nblk = delta_blocks_per_row(a);
     p.scale = a.scale;
     p.out = static_cast<uint8_t *>(out);
+    p.bwd = bwd;
     // as many heads of a group per CTA (they share [K; Q] K^T) as leave the GPU full
     const int64_t slots = delta_slots(a), R = a.nheads / a.ngroups;
     int hpc = (int)R;
@@ -345,7 +360,7 @@ cudaError_t launch_delta_prep(const ssm_delta_args &a, const SeqView &sv, const 
     auto kernel = a.dstate <= 64 ? delta_prep_kernel<64> : delta_prep_kernel<128>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, 128, smem, st>>>(p, tm_q, tm_k);
+    kernel<<<grid, 128, smem, st>>>(p, m.q, m.k);
     return cudaGetLastError();
 }
 

@@ -12,7 +12,29 @@ namespace dtc {
 constexpr int kQ = 64;                    // tokens per block
 constexpr uint32_t kTile = 8192;          // 64 rows x 64 bf16: one 128-byte-swizzled tile
 constexpr size_t kTBytes = 2 * kTile;     // T of one (block, head): high and low parts
-constexpr size_t kHeadBytes = 3 * kTile;  // ... and its attention weights
+// What the pre-pass leaves of one (block, head): T high, T low, attention weights
+// (high); for the backward also their low part.
+constexpr size_t kHeadBytes = 3 * kTile, kHeadBytesBwd = 4 * kTile;
+
+// What the backward keeps of one (block, head, 64-row slice), as operand tiles
+// of 128-byte rows: the entering state and the gradient of the leaving state
+// (64 rows x dstate, high parts), then dy, dR and u transposed (64 rows x 64
+// tokens).  Rows past headdim and tokens past the sequence are zero.
+struct Rec {
+    uint8_t *base;
+    int64_t state;                 // bytes of one state tile: 128 x dstate rounded up to 64
+    int nsl;
+    SSM_DEVINL uint8_t *at(int64_t slot, int64_t H, int head, int slice) const {
+        return base + ((slot * H + head) * nsl + slice) * (2 * state + 3 * (int64_t)kTile);
+    }
+    SSM_DEVINL int64_t dy() const { return 2 * state; }
+    SSM_DEVINL int64_t dR() const { return 2 * state + kTile; }
+    SSM_DEVINL int64_t u() const { return 2 * state + 2 * (int64_t)kTile; }
+};
+// beta of the backward: dbeta_i = dR_i . u_i / beta_i, and u_i / beta_i stays
+// exact for a beta so small that nothing else notices it.
+constexpr float kTinyBeta = 1e-20f;
+SSM_DEVINL float bwd_beta(float b) { return b == 0.f ? kTinyBeta : b; }
 
 // Wait for an mbarrier phase, at most two seconds; gives up as soon as another
 // thread of the CTA has (`abort`), and records the timeout in the error word.

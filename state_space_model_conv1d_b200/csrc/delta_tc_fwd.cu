@@ -32,12 +32,9 @@
 #include <string.h>
 
 #include "delta_tc.cuh"
+#include "delta_tc.h"
 
 namespace ssm {
-
-size_t delta_prep_bytes(const ssm_delta_args &a);
-cudaError_t launch_delta_prep(const ssm_delta_args &a, const SeqView &sv, const CUtensorMap &tm_q,
-                              const CUtensorMap &tm_k, void *out, cudaStream_t st);
 
 namespace {
 
@@ -86,7 +83,7 @@ template <int NK, bool DUAL> struct Lay {
     static constexpr uint32_t PM = T + 2 * kTPart, stage = PM + kTPart;
     static constexpr uint32_t Y = 2 * stage, AUX = Y + 2 * kTile;
     static constexpr size_t bytes = AUX + sizeof(Aux) + 1024;
-    static constexpr uint32_t tx = stage;
+    static constexpr uint32_t tx(bool st) { return st ? PM : stage; }
 };
 
 struct Args {
@@ -95,9 +92,12 @@ struct Args {
     const uint8_t *prep;           // delta_prep.cu: [slot][H][kHeadBytes]
     int64_t nblk;
     int R, nsl, units;             // heads per group, 64-row slices per head, CTAs per group
+    Rec rec;                       // the states' pass of the backward: where u and the states go
 };
 
-template <int NK, bool DUAL>
+// ST: the states' pass of the backward: no output, but every block's entering
+// state and u are kept (attention weights are neither loaded nor used).
+template <int NK, bool DUAL, bool ST>
 __global__ void __launch_bounds__(kThreads, 1)
 delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v) {
@@ -147,7 +147,7 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
     const int64_t slot0 = seq_slot(a.cu_seqlens, s, p.nblk);
     if (warp == 0) tc::tmem_alloc(&ax.tmem, kTmemCols);
     if (tid == 0) {
-        constexpr int kEmpty = 1 + kChainWarps + kOutWarps;
+        constexpr int kEmpty = 1 + kChainWarps + (ST ? 0 : kOutWarps);
         constexpr int counts[B_COUNT] = {
             1, 1, kEmpty, kEmpty, 1, 1,
             kChainWarps, kChainWarps, 1, kChainWarps, kChainWarps, 1, kChainWarps, kChainWarps, kChainWarps, 1,
@@ -179,6 +179,19 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
             __syncwarp();
             if (lane == 0) arrive(&ax.mb[b]);
         };
+        // the states' pass: values of this thread's row in a tile of block c, 16 bytes at a time
+        const int rr = (q & 1) * 32 + lane;
+        auto keep = [&](int c, int64_t off, int col, const float *v, int n8) {
+            if (half >= halves) return;
+            uint8_t *rec = p.rec.at(slot0 + c, H, head[half], row0[half] / 64);
+            for (int k = 0; k < n8; ++k) {
+                uint4 o = make_uint4(0, 0, 0, 0);
+                const float *f = v + 8 * k;
+                if (live) o = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+                const int cc = col + 8 * k;
+                *reinterpret_cast<uint4 *>(rec + off + (int64_t)(cc >> 6) * kTile + swz(rr, cc & 63)) = o;
+            }
+        };
         bool ok = wait(B_TAB0, 0);
         // the entering state: NK / 2 columns of this thread's row
 #pragma unroll 1
@@ -192,6 +205,7 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
                 v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
             }
             st_split16(tl + hop(cf, e >> 1, 0) + 8 * (e & 1), tl + hop(cf, e >> 1, 1) + 8 * (e & 1), v);
+            if (ST) keep(0, 0, c0, v, 2);
             const float d = ax.tab[0][half].total;
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] *= d;
@@ -273,14 +287,18 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
                 }
             }
             // u for the output, over the 32 columns of U that this warp has read
+            if constexpr (ST) {
+                keep(c, p.rec.u(), t0, x, 4);
+            } else {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t h[8];
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t h[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) h[i] = pack2(x[16 * b + 2 * i], x[16 * b + 2 * i + 1]);
-                tmem_st8(tl + TM_RU + t0 + 8 * b, h);
+                    for (int i = 0; i < 8; ++i) h[i] = pack2(x[16 * b + 2 * i], x[16 * b + 2 * i + 1]);
+                    tmem_st8(tl + TM_RU + t0 + 8 * b, h);
+                }
+                arrive_st(B_UOP);
             }
-            arrive_st(B_UOP);
             if (lane == 0) arrive(&ax.mb[B_EMPTY0 + stg]);
             // h
             const bool last = c + 1 == n;
@@ -317,6 +335,10 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
                 arrive_st(B_H0 + b);
             }
             if (NK == 64 && lane == 0) arrive(&ax.mb[B_H1]);
+            if (ST) {
+                keep(c + 1, 0, cf * (NK / 2), x, 4);
+                if (NK == 128) keep(c + 1, 0, cf * (NK / 2) + 32, h1, 4);
+            }
             // decayed for the next block's update; R, handed over later, covers these stores
 #pragma unroll
             for (int b = 0; b < NK / 64; ++b) {
@@ -335,7 +357,7 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
         __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + brow * a.y_batch_stride + lo * a.y_token_stride +
                            (int64_t)head[yh] * P + row0[yh] + (ch & 7) * 8;
         __nv_bfloat16 *ys = reinterpret_cast<__nv_bfloat16 *>(sm + L::Y);
-        for (int c = 0; c < n; ++c) {
+        for (int c = 0; !ST && c < n; ++c) {
             const uint32_t ph = c & 1;
             const int stg = c & 1, nt = (int)min((int64_t)kQ, hi - lo - (int64_t)c * kQ);
             float x[32];
@@ -394,7 +416,7 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
             const uint64_t dT = tc::desc_sw128(st + L::T, 16, 1024), dP = tc::desc_sw128(st + L::PM, 16, 1024);
             // h k and h q, once the last block's output has read h q and used u
             ok = wait(B_FULL0 + stg, (c >> 1) & 1) &&
-                 (c == 0 || (wait(B_HQ, ph ^ 1) && wait(B_M5, ph ^ 1)));
+                 (ST || c == 0 || (wait(B_HQ, ph ^ 1) && wait(B_M5, ph ^ 1)));
 #pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 ok = ok && wait(B_H0 + b, ph);
@@ -415,7 +437,7 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
                 __syncwarp();
             }
             // U = T R: (R high, T low), (R low, T high), (R high, T high)
-            ok = ok && (!DUAL || wait(B_HQ, ph));
+            ok = ok && (!DUAL || ST || wait(B_HQ, ph));
 #pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 ok = ok && wait(B_R0 + b, ph);
@@ -445,10 +467,12 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
                             mma_ts(tm + TM_H, tm + TM_OP + part * 32 + kk * 8, dKm + kk * 128, ID3, 1);
                     if (b) {
                         tc::mma_commit(&ax.mb[B_M3]);
+                        if (ST) tc::mma_commit(&ax.mb[B_EMPTY0 + stg]);
                     }
                 }
                 __syncwarp();
             }
+            if (ST) continue;
             // attention x u
             ok = ok && wait(B_UOP, ph) && wait(B_HQ, ph);
             if (!ok) break;
@@ -486,12 +510,13 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
                     const bool in = t < nt && (hh == 0 || head[1] != head[0]);
                     gv[hh][e] = in ? a.g[brow * a.g_batch_stride + (t0 + t) * a.g_token_stride + head[hh]] : 0.f;
                     bv[hh][e] = in ? a.beta[brow * a.beta_batch_stride + (t0 + t) * a.beta_token_stride + head[hh]] : 0.f;
+                    if (ST) bv[hh][e] = bwd_beta(bv[hh][e]);
                 }
             if (c >= 2 && !wait(B_EMPTY0 + stg, ((c >> 1) - 1) & 1)) break;
             uint8_t *st = sm + stg * L::stage;
             if (lane == 0) {
                 uint64_t *mb = &ax.mb[B_FULL0 + stg];
-                tc::mbar_expect_tx(mb, L::tx);
+                tc::mbar_expect_tx(mb, L::tx(ST));
 #pragma unroll
                 for (int x = 0; x < NK / 64; ++x) {
                     tma_load_4d(st + L::K + x * 2 * kTile, &tm_k, 64 * x, grp, (int)t0, (int)brow, mb);
@@ -503,9 +528,10 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
 #pragma unroll
                 for (int i = 0; i < (DUAL ? 2 : 1); ++i)
 #pragma unroll
-                    for (int part = 0; part < 3; ++part)       // T high, T low, attention weights
+                    for (int part = 0; part < (ST ? 2 : 3); ++part)       // T high, T low, attention weights
                         bulk_load(st + L::T + part * L::kTPart + i * kTile,
-                                  p.prep + ((slot0 + c) * H + head[i]) * kHeadBytes + part * kTile, kTile, mb);
+                                  p.prep + ((slot0 + c) * H + head[i]) * (ST ? kHeadBytesBwd : kHeadBytes) + part * kTile,
+                                  kTile, mb);
             }
             issued = c + 1;
 #pragma unroll
@@ -548,56 +574,75 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
     }
 }
 
-template <int NK, bool DUAL>
-cudaError_t run(const Args &p, dim3 grid, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(delta_fwd_kernel<NK, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int NK, bool DUAL, bool ST>
+cudaError_t run(const Args &p, dim3 grid, const DeltaMaps &m, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(delta_fwd_kernel<NK, DUAL, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Lay<NK, DUAL>::bytes);
     if (e != cudaSuccess) return e;
-    delta_fwd_kernel<NK, DUAL><<<grid, kThreads, Lay<NK, DUAL>::bytes, st>>>(p, q, k, v);
+    delta_fwd_kernel<NK, DUAL, ST><<<grid, kThreads, Lay<NK, DUAL>::bytes, st>>>(p, m.q, m.k, m.v);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 bool delta_tc_shape(const ssm_delta_args &a) {
-    return a.dtype == SSM_BF16 && a.dstate <= 128 && a.dstate % 8 == 0 && a.headdim % 8 == 0;
+    return a.dtype == SSM_BF16 && a.dstate <= 128 && a.dstate % 8 == 0 && a.headdim % 8 == 0 && a.nheads <= 65535;
 }
+namespace {
+bool al16(const void *p, int64_t bs = 0, int64_t ts = 0) { return ((uintptr_t)p % 16) == 0 && bs % 8 == 0 && ts % 8 == 0; }
+}  // namespace
 bool delta_tc_ok(const ssm_delta_args &a) {
-    auto al = [](const void *p, int64_t bs, int64_t ts) {
-        return ((uintptr_t)p % 16) == 0 && bs % 8 == 0 && ts % 8 == 0;
-    };
-    return delta_tc_shape(a) && a.seqlen > 0 && al(a.q, a.q_batch_stride, a.q_token_stride) &&
-           al(a.k, a.k_batch_stride, a.k_token_stride) && al(a.v, a.v_batch_stride, a.v_token_stride) &&
-           al(a.y, a.y_batch_stride, a.y_token_stride) && al(a.h0, 0, 0) && al(a.h_final, 0, 0);
+    return delta_tc_shape(a) && a.seqlen > 0 && al16(a.q, a.q_batch_stride, a.q_token_stride) &&
+           al16(a.k, a.k_batch_stride, a.k_token_stride) && al16(a.v, a.v_batch_stride, a.v_token_stride) &&
+           al16(a.y, a.y_batch_stride, a.y_token_stride) && al16(a.h0) && al16(a.h_final);
 }
-size_t delta_tc_workspace_bytes(const ssm_delta_args &a) { return delta_prep_bytes(a); }
+bool delta_tc_bwd_ok(const ssm_delta_bwd_args &b) {
+    ssm_delta_args f = b.fwd;
+    f.y = const_cast<void *>(b.dy);
+    f.y_batch_stride = b.dy_batch_stride;
+    f.y_token_stride = b.dy_token_stride;
+    f.h_final = nullptr;
+    return delta_tc_ok(f) && al16(b.dh_final) && al16(b.dq) && al16(b.dk) && al16(b.dv) && al16(b.dh0);
+}
+size_t delta_tc_workspace_bytes(const ssm_delta_args &a) { return delta_prep_bytes(a, false); }
 
-cudaError_t launch_delta_tc(const ssm_delta_args &a, const SeqView &sv, void *ws, cudaStream_t st) {
-    const int64_t nseq = a.cu_seqlens ? a.nseqs : a.batch;
-    if (nseq == 0) return cudaSuccess;
+bool delta_maps(const ssm_delta_args &a, DeltaMaps *m) {
+    const int64_t rows = a.cu_seqlens ? 1 : a.batch, hp = a.nheads * a.headdim;
+    return make_map_group(&m->q, a.q, a.dstate, a.ngroups, a.seqlen, rows, a.q_token_stride, a.q_batch_stride) &&
+           make_map_group(&m->k, a.k, a.dstate, a.ngroups, a.seqlen, rows, a.k_token_stride, a.k_batch_stride) &&
+           make_map_box(&m->v, a.v, hp, a.seqlen, rows, a.seqlen > 1 ? a.v_token_stride : hp, a.v_batch_stride, false,
+                        dtc::kQ);
+}
+
+cudaError_t launch_delta_chain(const ssm_delta_args &a, const SeqView &sv, const DeltaMaps &m, const void *prep,
+                               const dtc::Rec *rec, cudaStream_t st) {
     Args p;
     p.a = a;
     p.sv = sv;
-    p.prep = static_cast<const uint8_t *>(ws);
+    p.prep = static_cast<const uint8_t *>(prep);
     p.nblk = delta_blocks_per_row(a);
     p.R = (int)(a.nheads / a.ngroups);
     p.nsl = (int)((a.headdim + 63) / 64);
     p.units = (p.R * p.nsl + 1) / 2;
-    const int64_t rows = a.cu_seqlens ? 1 : a.batch;
-    CUtensorMap q, k, v;
-    if (!make_map_group(&q, a.q, a.dstate, a.ngroups, a.seqlen, rows, a.q_token_stride, a.q_batch_stride) ||
-        !make_map_group(&k, a.k, a.dstate, a.ngroups, a.seqlen, rows, a.k_token_stride, a.k_batch_stride) ||
-        !make_map_box(&v, a.v, a.nheads * a.headdim, a.seqlen, rows,
-                      a.seqlen > 1 ? a.v_token_stride : a.nheads * a.headdim, a.v_batch_stride, false, kQ))
-        return cudaErrorInvalidValue;
-    cudaError_t e = launch_delta_prep(a, sv, q, k, ws, st);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(a.ngroups * p.units), (unsigned)nseq);
+    p.rec = rec ? *rec : dtc::Rec{nullptr, 0, 1};
+    const dim3 grid((unsigned)(a.ngroups * p.units), (unsigned)(a.cu_seqlens ? a.nseqs : a.batch));
     const bool dual = p.nsl % 2 != 0;
+    if (rec) {
+        if (a.dstate <= 64) return dual ? run<64, true, true>(p, grid, m, st) : run<64, false, true>(p, grid, m, st);
+        return dual ? run<128, true, true>(p, grid, m, st) : run<128, false, true>(p, grid, m, st);
+    }
+    if (a.dstate <= 64) return dual ? run<64, true, false>(p, grid, m, st) : run<64, false, false>(p, grid, m, st);
+    return dual ? run<128, true, false>(p, grid, m, st) : run<128, false, false>(p, grid, m, st);
+}
+
+cudaError_t launch_delta_tc(const ssm_delta_args &a, const SeqView &sv, void *ws, cudaStream_t st) {
+    if ((a.cu_seqlens ? a.nseqs : a.batch) == 0) return cudaSuccess;
+    DeltaMaps m;
+    if (!delta_maps(a, &m)) return cudaErrorInvalidValue;
+    cudaError_t e = launch_delta_prep(a, sv, m, ws, false, st);
+    if (e != cudaSuccess) return e;
     timing_begin(st);
-    if (a.dstate <= 64) e = dual ? run<64, true>(p, grid, q, k, v, st) : run<64, false>(p, grid, q, k, v, st);
-    else e = dual ? run<128, true>(p, grid, q, k, v, st) : run<128, false>(p, grid, q, k, v, st);
+    e = launch_delta_chain(a, sv, m, ws, nullptr, st);
     timing_end(st);
     return e;
 }

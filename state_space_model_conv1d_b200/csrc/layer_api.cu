@@ -139,7 +139,8 @@ ssm_status ssm_delta_fwd(const ssm_delta_args *args, void *workspace, size_t ws_
 
 size_t ssm_delta_bwd_workspace_size(const ssm_delta_bwd_args *args) {
     if (!args || !sizes_ok(args->fwd)) return 0;
-    return delta_prefix(args->fwd) + ssm::delta_simt_bwd_workspace_bytes(*args);
+    return delta_prefix(args->fwd) + (ssm::delta_tc_bwd_ok(*args) ? ssm::delta_tc_bwd_workspace_bytes(*args)
+                                                                  : ssm::delta_simt_bwd_workspace_bytes(*args));
 }
 
 ssm_status ssm_delta_bwd(const ssm_delta_bwd_args *args, void *workspace, size_t ws_bytes, void *stream) {
@@ -150,7 +151,9 @@ ssm_status ssm_delta_bwd(const ssm_delta_bwd_args *args, void *workspace, size_t
     char *ws = static_cast<char *>(workspace);
     ssm::SeqView sv;
     SSM_TRY(delta_plan(args->fwd, ws, st, &sv));
-    return cuda_status(ssm::launch_delta_simt_bwd(*args, sv, ws + delta_prefix(args->fwd), st));
+    ws += delta_prefix(args->fwd);
+    if (ssm::delta_tc_bwd_ok(*args)) return cuda_status(ssm::launch_delta_tc_bwd(*args, sv, ws, st));
+    return cuda_status(ssm::launch_delta_simt_bwd(*args, sv, ws, st));
 }
 
 ssm_status ssm_delta_update(const ssm_delta_update_args *a, void *stream) {
