@@ -24,10 +24,12 @@
 namespace ssm {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kRows = kWarps * 4;      // state rows per CTA
-constexpr int kTok = kDeltaCkpt;       // tokens staged at a time
+// W warps per CTA: 8 (32 state rows), or 2 (8 rows) where CTAs of 8 would leave
+// SMs idle; a token's row of k and q is read from shared memory by every warp,
+// and with 8 warps on one SM that bounds the token (2 x 333 tokens, 6 heads,
+// P 40, N 72: 166 us with 8, 75 us with 2).
+template <int W> constexpr int threads_of() { return W * 32; }
+template <int W> constexpr int rows_of() { return W * 4; }
 
 struct Args {
     ssm_delta_args a;
@@ -61,15 +63,36 @@ SSM_DEVINL Seq find_seq(const ssm_delta_args &a, const SeqView &sv, int y) {
 // State index of element e of this lane: 4 consecutive of every 32.
 SSM_DEVINL int state_of(int lane8, int e) { return (e >> 2) * 32 + lane8 * 4 + (e & 3); }
 
-// Stage `nt` tokens of a [tokens][width] operand as fp32, `pad` columns wide
-// (zeros past width and behind nt).
-template <typename T>
-SSM_DEVINL void stage(float *dst, int pad, const T *src, int64_t ts, int nt, int width) {
-    for (int i = threadIdx.x; i < kTok * pad; i += kThreads) {
-        const int t = i / pad, c = i % pad;
-        dst[i] = (t < nt && c < width) ? Elem<T>::ld(src + (int64_t)t * ts + c) : 0.f;
+// `nt` tokens of a [tokens][width] operand on the way to shared memory, fp32,
+// PAD columns wide (zeros past width and behind nt): all of a thread's loads
+// are issued together, while the tokens before are still in work.
+template <typename T, int PAD, int kTok, int kThreads> struct Staged {
+    static constexpr int kPer = kTok * PAD / kThreads;
+    float v[kPer];
+    SSM_DEVINL void load(const T *src, int64_t ts, int nt, int width) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            // (token and column without a division wherever one count divides the other)
+            int t, c;
+            if constexpr (PAD % kThreads == 0) {
+                t = i * kThreads / PAD;
+                c = threadIdx.x + i * kThreads % PAD;
+            } else if constexpr (kThreads % PAD == 0) {
+                t = threadIdx.x / PAD + i * (kThreads / PAD);
+                c = threadIdx.x % PAD;
+            } else {
+                const int x = threadIdx.x + i * kThreads;
+                t = x / PAD;
+                c = x % PAD;
+            }
+            v[i] = (t < nt && c < width) ? Elem<T>::ld(src + (int64_t)t * ts + c) : 0.f;
+        }
     }
-}
+    SSM_DEVINL void store(float *dst) const {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) dst[threadIdx.x + i * kThreads] = v[i];
+    }
+};
 SSM_DEVINL float decay_of(float g) { return expf(fmaxf(g, kMinLogDecay)); }
 
 template <int NE>
@@ -87,13 +110,16 @@ SSM_DEVINL float sum8(float v) {
     return v;
 }
 
-template <typename T, int NE>
-__global__ void __launch_bounds__(kThreads) delta_scan_kernel(const Args p) {
+template <int W> constexpr int fwd_tokens() { return W == 8 ? 32 : 8; }    // tokens staged at a time
+
+template <typename T, int NE, int W>
+__global__ void __launch_bounds__(threads_of<W>()) delta_scan_kernel(const Args p) {
+    constexpr int kThreads = threads_of<W>(), kRows = rows_of<W>(), kTok = fwd_tokens<W>();
     const ssm_delta_args &a = p.a;
     if (p.sv.err && *p.sv.err != 0) return;
     constexpr int NP = NE * 8;
     extern __shared__ float sm[];
-    float *ks = sm, *qs = ks + kTok * NP, *vs = qs + kTok * NP, *as = vs + kTok * kRows, *bs = as + kTok, *kq = bs + kTok;
+    float *ks = sm, *qs = ks + kTok * NP, *vs = qs + kTok * NP, *as = vs + kTok * kRows, *bs = as + kTok;
     const Seq sq = find_seq(a, p.sv, blockIdx.y);
     const int64_t H = a.nheads, P = a.headdim, N = a.dstate;
     const int h = blockIdx.x % H, p0 = (int)(blockIdx.x / H) * kRows;
@@ -115,37 +141,42 @@ __global__ void __launch_bounds__(kThreads) delta_scan_kernel(const Args p) {
     const float *g = a.g + sq.row * a.g_batch_stride + h, *be = a.beta + sq.row * a.beta_batch_stride + h;
     T *y = a.y ? (T *)a.y + sq.row * a.y_batch_stride + h * P + p0 : nullptr;
     const int vw = (int)min((int64_t)kRows, P - p0);
+    Staged<T, NP, kTok, kThreads> sk_, sq_s;
+    Staged<T, kRows, kTok, kThreads> sv_;
+    float ga = 1.f, gb = 0.f;
+    const auto fetch = [&](int64_t t0) {
+        const int nt = (int)min((int64_t)kTok, sq.hi - t0);
+        sk_.load(k + t0 * a.k_token_stride, a.k_token_stride, nt, (int)N);
+        if (y) sq_s.load(q + t0 * a.q_token_stride, a.q_token_stride, nt, (int)N);
+        sv_.load(v + t0 * a.v_token_stride, a.v_token_stride, nt, vw);
+        if (threadIdx.x < kTok) {
+            const int t = threadIdx.x;
+            ga = t < nt ? g[(t0 + t) * a.g_token_stride] : 0.f;
+            gb = t < nt ? be[(t0 + t) * a.beta_token_stride] : 0.f;
+        }
+    };
+    if (sq.lo < sq.hi) fetch(sq.lo);
     for (int64_t t0 = sq.lo; t0 < sq.hi; t0 += kTok) {
         const int nt = (int)min((int64_t)kTok, sq.hi - t0);
-        if (p.ckpt && live) {
+        if (p.ckpt && live && (t0 - sq.lo) % kDeltaCkpt == 0) {
             float *c = p.ckpt + (((sq.ckpt_row + (t0 - sq.lo) / kDeltaCkpt) * H + h) * P + p0 + r) * N;
 #pragma unroll
             for (int e = 0; e < NE; ++e)
                 if (state_of(lane8, e) < N) c[state_of(lane8, e)] = st[e];
         }
         __syncthreads();                               // the tokens before are read
-        stage(ks, NP, k + t0 * a.k_token_stride, a.k_token_stride, nt, (int)N);
-        if (y) stage(qs, NP, q + t0 * a.q_token_stride, a.q_token_stride, nt, (int)N);
-        stage(vs, kRows, v + t0 * a.v_token_stride, a.v_token_stride, nt, vw);
+        sk_.store(ks);
+        if (y) sq_s.store(qs);
+        sv_.store(vs);
         if (threadIdx.x < kTok) {
-            const int t = threadIdx.x;
-            as[t] = t < nt ? decay_of(g[(t0 + t) * a.g_token_stride]) : 1.f;
-            bs[t] = t < nt ? be[(t0 + t) * a.beta_token_stride] : 0.f;
+            as[threadIdx.x] = decay_of(ga);
+            bs[threadIdx.x] = gb;
         }
         __syncthreads();
-        if (y) {
-            for (int t = warp; t < nt; t += kWarps) {
-                float s = 0.f;
-                for (int n = lane; n < NP; n += 32) s = fmaf(ks[t * NP + n], qs[t * NP + n], s);
-#pragma unroll
-                for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-                if (lane == 0) kq[t] = s;
-            }
-            __syncthreads();
-        }
+        if (t0 + kTok < sq.hi) fetch(t0 + kTok);
         for (int t = 0; t < nt; ++t) {
             const float al = as[t];
-            float sk = 0.f, sq_ = 0.f, kk[NE];
+            float sk2[2] = {0.f, 0.f}, sq2[2] = {0.f, 0.f}, kq = 0.f, kk[NE];        // two chains a sum
 #pragma unroll
             for (int e = 0; e < NE; e += 4) {
                 const float4 k4 = *reinterpret_cast<const float4 *>(ks + t * NP + state_of(lane8, e));
@@ -154,25 +185,29 @@ __global__ void __launch_bounds__(kThreads) delta_scan_kernel(const Args p) {
 #pragma unroll
             for (int e = 0; e < NE; ++e) {
                 st[e] *= al;
-                sk = fmaf(st[e], kk[e], sk);
+                sk2[e & 1] = fmaf(st[e], kk[e], sk2[e & 1]);
             }
             if (y) {
 #pragma unroll
                 for (int e = 0; e < NE; e += 4) {
                     const float4 q4 = *reinterpret_cast<const float4 *>(qs + t * NP + state_of(lane8, e));
-                    sq_ = fmaf(st[e], q4.x, sq_);
-                    sq_ = fmaf(st[e + 1], q4.y, sq_);
-                    sq_ = fmaf(st[e + 2], q4.z, sq_);
-                    sq_ = fmaf(st[e + 3], q4.w, sq_);
+                    sq2[0] = fmaf(st[e], q4.x, sq2[0]);
+                    sq2[1] = fmaf(st[e + 1], q4.y, sq2[1]);
+                    sq2[0] = fmaf(st[e + 2], q4.z, sq2[0]);
+                    sq2[1] = fmaf(st[e + 3], q4.w, sq2[1]);
+                    kq = fmaf(kk[e], q4.x, kq);
+                    kq = fmaf(kk[e + 1], q4.y, kq);
+                    kq = fmaf(kk[e + 2], q4.z, kq);
+                    kq = fmaf(kk[e + 3], q4.w, kq);
                 }
-                sq_ = sum8(sq_);
             }
-            sk = sum8(sk);
+            const float sk = sum8(sk2[0] + sk2[1]), sq_ = y ? sum8(sq2[0] + sq2[1]) : 0.f;
+            if (y) kq = sum8(kq);
             const float u = bs[t] * (vs[t * kRows + r] - sk);
 #pragma unroll
             for (int e = 0; e < NE; ++e) st[e] = fmaf(u, kk[e], st[e]);
             if (y && lane8 == 0 && live)
-                Elem<T>::st(y + (t0 + t) * a.y_token_stride + r, a.scale * fmaf(u, kq[t], sq_));
+                Elem<T>::st(y + (t0 + t) * a.y_token_stride + r, a.scale * fmaf(u, kq, sq_));
         }
     }
     if (a.h_final && live) {
@@ -211,8 +246,9 @@ SSM_DEVINL void rows_sum(float (&x)[NE], float (&out)[NE / 4], int lane) {
 }
 
 // TR tokens are held in registers at a time (TR * NE states each).
-template <typename T, int NE, int TR>
-__global__ void __launch_bounds__(kThreads, 1) delta_scan_bwd_kernel(const BwdArgs p) {
+template <typename T, int NE, int TR, int W>
+__global__ void __launch_bounds__(threads_of<W>(), 1) delta_scan_bwd_kernel(const BwdArgs p) {
+    constexpr int kThreads = threads_of<W>(), kRows = rows_of<W>(), kTok = kDeltaCkpt, kWarps = W;
     const ssm_delta_args &a = p.b.fwd;
     if (p.sv.err && *p.sv.err != 0) return;
     constexpr int NP = NE * 8;
@@ -252,10 +288,18 @@ __global__ void __launch_bounds__(kThreads, 1) delta_scan_bwd_kernel(const BwdAr
         const int64_t t0 = sq.lo + c * kTok;
         const int nt = (int)min((int64_t)kTok, sq.hi - t0);
         __syncthreads();
-        stage(ks, NP, k + t0 * a.k_token_stride, a.k_token_stride, nt, (int)N);
-        stage(qs, NP, q + t0 * a.q_token_stride, a.q_token_stride, nt, (int)N);
-        stage(vs, kRows, v + t0 * a.v_token_stride, a.v_token_stride, nt, vw);
-        stage(ds_, kRows, dy + t0 * p.b.dy_token_stride, p.b.dy_token_stride, nt, vw);
+        {
+            Staged<T, NP, kTok, kThreads> s;
+            s.load(k + t0 * a.k_token_stride, a.k_token_stride, nt, (int)N);
+            Staged<T, kRows, kTok, kThreads> s2, s3;
+            s2.load(v + t0 * a.v_token_stride, a.v_token_stride, nt, vw);
+            s3.load(dy + t0 * p.b.dy_token_stride, p.b.dy_token_stride, nt, vw);
+            s.store(ks);
+            s2.store(vs);
+            s3.store(ds_);
+            s.load(q + t0 * a.q_token_stride, a.q_token_stride, nt, (int)N);
+            s.store(qs);
+        }
         if (threadIdx.x < kTok) {
             const int t = threadIdx.x;
             as[t] = t < nt ? decay_of(g[(t0 + t) * a.g_token_stride]) : 1.f;
@@ -413,26 +457,48 @@ cudaError_t set_smem(K kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, int NE>
-cudaError_t run_fwd(const Args &p, dim3 grid, cudaStream_t st) {
-    const size_t smem = (size_t)(2 * kTok * NE * 8 + kTok * kRows + 3 * kTok) * 4;
-    cudaError_t e = set_smem(delta_scan_kernel<T, NE>, smem);
+template <typename T, int NE, int W>
+cudaError_t run_fwd(const Args &p, cudaStream_t st) {
+    constexpr int kTok = fwd_tokens<W>();
+    const ssm_delta_args &a = p.a;
+    const dim3 grid((unsigned)(a.nheads * ((a.headdim + rows_of<W>() - 1) / rows_of<W>())),
+                    (unsigned)(a.cu_seqlens ? a.nseqs : a.batch));
+    const size_t smem = (size_t)(2 * kTok * NE * 8 + kTok * rows_of<W>() + 2 * kTok) * 4;
+    cudaError_t e = set_smem(delta_scan_kernel<T, NE, W>, smem);
     if (e != cudaSuccess) return e;
-    delta_scan_kernel<T, NE><<<grid, kThreads, smem, st>>>(p);
+    delta_scan_kernel<T, NE, W><<<grid, threads_of<W>(), smem, st>>>(p);
     return cudaGetLastError();
+}
+template <typename T, int NE, int TR, int W>
+cudaError_t run_bwd(const BwdArgs &p, cudaStream_t st) {
+    constexpr int kTok = kDeltaCkpt;
+    const ssm_delta_args &a = p.b.fwd;
+    const dim3 grid((unsigned)(a.nheads * ((a.headdim + rows_of<W>() - 1) / rows_of<W>())),
+                    (unsigned)(a.cu_seqlens ? a.nseqs : a.batch));
+    const size_t smem =
+        (size_t)(2 * kTok * NE * 8 + 2 * kTok * rows_of<W>() + 2 * kTok + 2 * TR * W * NE * 8 + 2 * TR * W) * 4;
+    cudaError_t e = set_smem(delta_scan_bwd_kernel<T, NE, TR, W>, smem);
+    if (e != cudaSuccess) return e;
+    delta_scan_bwd_kernel<T, NE, TR, W><<<grid, threads_of<W>(), smem, st>>>(p);
+    return cudaGetLastError();
+}
+template <typename T, int NE>
+cudaError_t pick_fwd(const Args &p, int w, cudaStream_t st) {
+    return w == 8 ? run_fwd<T, NE, 8>(p, st) : run_fwd<T, NE, 2>(p, st);
 }
 template <typename T, int NE, int TR>
-cudaError_t run_bwd(const BwdArgs &p, dim3 grid, cudaStream_t st) {
-    const size_t smem =
-        (size_t)(2 * kTok * NE * 8 + 2 * kTok * kRows + 2 * kTok + 2 * TR * kWarps * NE * 8 + 2 * TR * kWarps) * 4;
-    cudaError_t e = set_smem(delta_scan_bwd_kernel<T, NE, TR>, smem);
-    if (e != cudaSuccess) return e;
-    delta_scan_bwd_kernel<T, NE, TR><<<grid, kThreads, smem, st>>>(p);
-    return cudaGetLastError();
+cudaError_t pick_bwd(const BwdArgs &p, int w, cudaStream_t st) {
+    return w == 8 ? run_bwd<T, NE, TR, 8>(p, st) : run_bwd<T, NE, TR, 2>(p, st);
 }
 
-int64_t slices_of(const ssm_delta_args &a) { return (a.headdim + kRows - 1) / kRows; }
 int64_t seqs_of(const ssm_delta_args &a) { return a.cu_seqlens ? a.nseqs : a.batch; }
+int warps_of(const ssm_delta_args &a) {
+    return seqs_of(a) * a.nheads * ((a.headdim + rows_of<8>() - 1) / rows_of<8>()) < sm_count() ? 2 : 8;
+}
+int64_t slices_of(const ssm_delta_args &a) {
+    const int rows = warps_of(a) * 4;
+    return (a.headdim + rows - 1) / rows;
+}
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
@@ -440,11 +506,13 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 cudaError_t launch_delta_simt(const ssm_delta_args &a, const SeqView &sv, float *ckpt, cudaStream_t st) {
     if (seqs_of(a) == 0) return cudaSuccess;
     const Args p{a, sv, ckpt};
-    const dim3 grid((unsigned)(a.nheads * slices_of(a)), (unsigned)seqs_of(a));
+    const int w = warps_of(a);
     const bool bf = a.dtype == SSM_BF16;
-    if (a.dstate <= 64) return bf ? run_fwd<__nv_bfloat16, 8>(p, grid, st) : run_fwd<float, 8>(p, grid, st);
-    if (a.dstate <= 128) return bf ? run_fwd<__nv_bfloat16, 16>(p, grid, st) : run_fwd<float, 16>(p, grid, st);
-    return bf ? run_fwd<__nv_bfloat16, 32>(p, grid, st) : run_fwd<float, 32>(p, grid, st);
+    if (a.dstate <= 32) return bf ? pick_fwd<__nv_bfloat16, 4>(p, w, st) : pick_fwd<float, 4>(p, w, st);
+    if (a.dstate <= 64) return bf ? pick_fwd<__nv_bfloat16, 8>(p, w, st) : pick_fwd<float, 8>(p, w, st);
+    if (a.dstate <= 96) return bf ? pick_fwd<__nv_bfloat16, 12>(p, w, st) : pick_fwd<float, 12>(p, w, st);
+    if (a.dstate <= 128) return bf ? pick_fwd<__nv_bfloat16, 16>(p, w, st) : pick_fwd<float, 16>(p, w, st);
+    return bf ? pick_fwd<__nv_bfloat16, 32>(p, w, st) : pick_fwd<float, 32>(p, w, st);
 }
 
 size_t delta_simt_bwd_workspace_bytes(const ssm_delta_bwd_args &b) {
@@ -457,25 +525,27 @@ size_t delta_simt_bwd_workspace_bytes(const ssm_delta_bwd_args &b) {
 cudaError_t launch_delta_simt_bwd(const ssm_delta_bwd_args &b, const SeqView &sv, void *ws, cudaStream_t st) {
     const ssm_delta_args &a = b.fwd;
     if (seqs_of(a) == 0) return cudaSuccess;
-    char *w = static_cast<char *>(ws);
-    float *ckpt = reinterpret_cast<float *>(w);
-    w += up256((size_t)delta_ckpt_rows(a) * a.nheads * a.headdim * a.dstate * 4);
+    char *at = static_cast<char *>(ws);
+    float *ckpt = reinterpret_cast<float *>(at);
+    at += up256((size_t)delta_ckpt_rows(a) * a.nheads * a.headdim * a.dstate * 4);
     const size_t tok = (size_t)(a.batch * a.seqlen) * a.nheads * slices_of(a) * 4;
     BwdArgs p{b, sv, ckpt, nullptr, nullptr, nullptr, nullptr};
-    p.pq = reinterpret_cast<float *>(w); w += up256(tok * a.dstate);
-    p.pk = reinterpret_cast<float *>(w); w += up256(tok * a.dstate);
-    p.pg = reinterpret_cast<float *>(w); w += up256(tok);
-    p.pb = reinterpret_cast<float *>(w);
+    p.pq = reinterpret_cast<float *>(at); at += up256(tok * a.dstate);
+    p.pk = reinterpret_cast<float *>(at); at += up256(tok * a.dstate);
+    p.pg = reinterpret_cast<float *>(at); at += up256(tok);
+    p.pb = reinterpret_cast<float *>(at);
     ssm_delta_args f = a;
     f.y = nullptr;
     f.h_final = nullptr;
     cudaError_t e = launch_delta_simt(f, sv, ckpt, st);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(a.nheads * slices_of(a)), (unsigned)seqs_of(a));
+    const int w = warps_of(a);
     const bool bf = a.dtype == SSM_BF16;
-    if (a.dstate <= 64) e = bf ? run_bwd<__nv_bfloat16, 8, 8>(p, grid, st) : run_bwd<float, 8, 8>(p, grid, st);
-    else if (a.dstate <= 128) e = bf ? run_bwd<__nv_bfloat16, 16, 8>(p, grid, st) : run_bwd<float, 16, 8>(p, grid, st);
-    else e = bf ? run_bwd<__nv_bfloat16, 32, 4>(p, grid, st) : run_bwd<float, 32, 4>(p, grid, st);
+    if (a.dstate <= 32) e = bf ? pick_bwd<__nv_bfloat16, 4, 8>(p, w, st) : pick_bwd<float, 4, 8>(p, w, st);
+    else if (a.dstate <= 64) e = bf ? pick_bwd<__nv_bfloat16, 8, 8>(p, w, st) : pick_bwd<float, 8, 8>(p, w, st);
+    else if (a.dstate <= 96) e = bf ? pick_bwd<__nv_bfloat16, 12, 8>(p, w, st) : pick_bwd<float, 12, 8>(p, w, st);
+    else if (a.dstate <= 128) e = bf ? pick_bwd<__nv_bfloat16, 16, 8>(p, w, st) : pick_bwd<float, 16, 8>(p, w, st);
+    else e = bf ? pick_bwd<__nv_bfloat16, 32, 4>(p, w, st) : pick_bwd<float, 32, 4>(p, w, st);
     if (e != cudaSuccess) return e;
     const int64_t work = a.batch * a.seqlen * a.ngroups * a.dstate;
     if (work == 0) return cudaSuccess;
