@@ -16,10 +16,15 @@ constexpr size_t kTBytes = 2 * kTile;     // T of one (block, head): high and lo
 // (high); for the backward also their low part.
 constexpr size_t kHeadBytes = 3 * kTile, kHeadBytesBwd = 4 * kTile;
 
-// What the backward keeps of one (block, head, 64-row slice), as operand tiles
-// of 128-byte rows: the entering state and the gradient of the leaving state
-// (64 rows x dstate, high parts), then dy, dR and u transposed (64 rows x 64
-// tokens).  Rows past headdim and tokens past the sequence are zero.
+// What the backward keeps of one (block, head, 64-row slice): the entering state
+// and the gradient of the leaving state (64 rows x dstate, high parts), then
+// dy, dR and u transposed (64 rows x 64 tokens).  Rows past headdim and tokens
+// past the sequence are zero.  16 bytes of a row (8 columns) lie beside those
+// of the next row: a warp, a row in each lane, writes whole lines (in rows of
+// 128 bytes the same stores took a line each and were the chain's bound), and
+// the tile is an unswizzled MN-major operand as it stands: 8 columns every
+// 1024 bytes, 8 rows every 128.
+SSM_DEVINL uint32_t rec_off(int row, int col) { return (uint32_t)(col >> 3) * 1024u + (uint32_t)row * 16u; }
 struct Rec {
     uint8_t *base;
     int64_t state;                 // bytes of one state tile: 128 x dstate rounded up to 64

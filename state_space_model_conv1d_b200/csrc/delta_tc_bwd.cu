@@ -176,8 +176,7 @@ delta_bwd_chain_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, c
                 uint4 o = make_uint4(0, 0, 0, 0);
                 const float *f = v + 8 * k;
                 if (live) o = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-                const int cc = col + 8 * k;
-                *reinterpret_cast<uint4 *>(rec + (int64_t)(cc >> 6) * kTile + swz(rr, cc & 63)) = o;
+                *reinterpret_cast<uint4 *>(rec + rec_off(rr, col + 8 * k)) = o;
             }
         };
         bool ok = wait(B_TAB0, 0);
@@ -339,7 +338,7 @@ delta_bwd_chain_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, c
                 uint8_t *rec = p.rec.at(slot0 + n - 1 - it, H, head[half], row0[half] / 64) + p.rec.dy();
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    *reinterpret_cast<uint4 *>(rec + swz(rr, 8 * k)) =
+                    *reinterpret_cast<uint4 *>(rec + rec_off(rr, 8 * k)) =
                         make_uint4(dy[4 * k], dy[4 * k + 1], dy[4 * k + 2], dy[4 * k + 3]);
             }
             return true;
@@ -373,26 +372,37 @@ delta_bwd_chain_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, c
             // dR: dv = beta dR by way of shared memory, and dR itself for the last launch
             ok = ok && wait(B_DR, ph);
             tc::fence_after_sync();
+            float x[2][32];
+            uint32_t r0[32], r1[32];
+            tmem_ld32_start(tl + TM_X1 + (DUAL && half ? 64 : 0), r0);
+            tmem_ld32_start(tl + TM_X1 + (DUAL && half ? 64 : 0) + 32, r1);
+            tmem_ld32_wait(r0, x[0]);
+            tmem_ld32_wait(r1, x[1]);
+            tc::fence_before_sync();
+            arrive_w(B_RREAD);
             uint8_t *rec = p.rec.at(slot0 + n - 1 - it, H, head[half], row0[half] / 64) + p.rec.dR();
-#pragma unroll 1
+#pragma unroll
             for (int b = 0; b < 2; ++b) {
-                float x[32];
-                tc::tmem_ld32(tl + TM_X1 + (DUAL && half ? 64 : 0) + 32 * b, x);
+                const float *f = x[b];
                 if (half < halves && ok)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint4 o = make_uint4(0, 0, 0, 0);
                         if (live)
-                            o = make_uint4(pack2(x[8 * k], x[8 * k + 1]), pack2(x[8 * k + 2], x[8 * k + 3]),
-                                           pack2(x[8 * k + 4], x[8 * k + 5]), pack2(x[8 * k + 6], x[8 * k + 7]));
-                        *reinterpret_cast<uint4 *>(rec + swz(rr, 32 * b + 8 * k)) = o;
+                            o = make_uint4(pack2(f[8 * k], f[8 * k + 1]), pack2(f[8 * k + 2], f[8 * k + 3]),
+                                           pack2(f[8 * k + 4], f[8 * k + 5]), pack2(f[8 * k + 6], f[8 * k + 7]));
+                        *reinterpret_cast<uint4 *>(rec + rec_off(rr, 32 * b + 8 * k)) = o;
                     }
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    vs[(32 * b + i) * 128 + 32 * q + lane] = __float2bfloat16_rn(tb.beta[32 * b + i] * x[i]);
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 be = *reinterpret_cast<const float4 *>(tb.beta + 32 * b + i);
+                    __nv_bfloat16 *at = vs + (32 * b + i) * 128 + 32 * q + lane;
+                    at[0] = __float2bfloat16_rn(be.x * f[i]);
+                    at[128] = __float2bfloat16_rn(be.y * f[i + 1]);
+                    at[256] = __float2bfloat16_rn(be.z * f[i + 2]);
+                    at[384] = __float2bfloat16_rn(be.w * f[i + 3]);
+                }
             }
-            tc::fence_before_sync();
-            arrive_w(B_RREAD);
             if (lane == 0) arrive(&ax.mb[B_EMPTY0 + stg]);
             if (!bar_all<128>(ok)) break;
             if (in) {
@@ -743,12 +753,11 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
                 tc::fence_after_sync();
                 for (int x = 0; x < ns; ++x) {
                     const uint32_t rec = sb + L::REC + x * L::rec;
-                    const uint64_t dH = tc::desc_sw128(rec, kTile, 1024), dD = tc::desc_sw128(rec + L::kAtoms * kTile, kTile, 1024);
-                    const uint64_t dY = tc::desc_sw128(rec + 2 * L::kAtoms * kTile, kTile, 1024), dR = dY + (kTile >> 4),
-                                   dU = dR + (kTile >> 4);
+                    const uint64_t dH = tc::desc(rec, 128, 1024), dD = dH + (L::kAtoms * kTile >> 4);
+                    const uint64_t dY = dD + (L::kAtoms * kTile >> 4), dR = dY + (kTile >> 4), dU = dR + (kTile >> 4);
 #pragma unroll 1
                     for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t o = kk * 128, c = s0 + x + kk > 0;
+                        const uint32_t o = kk * 16, c = s0 + x + kk > 0;
                         tc::mma_bf16(tm + TG_U, dY + o, dU + o, tc::idesc_bf16(128, 64, 1, 1), c);
                         tc::mma_bf16(tm + TG_H, dY + o, dH + o, tc::idesc_bf16(128, NK, 1, 1), c);
                         tc::mma_bf16(tm + TG_D, dR + o, dD + o, tc::idesc_bf16(128, NK, 1, 1), c);

@@ -188,8 +188,7 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
                 uint4 o = make_uint4(0, 0, 0, 0);
                 const float *f = v + 8 * k;
                 if (live) o = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-                const int cc = col + 8 * k;
-                *reinterpret_cast<uint4 *>(rec + off + (int64_t)(cc >> 6) * kTile + swz(rr, cc & 63)) = o;
+                *reinterpret_cast<uint4 *>(rec + off + rec_off(rr, col + 8 * k)) = o;
             }
         };
         bool ok = wait(B_TAB0, 0);
