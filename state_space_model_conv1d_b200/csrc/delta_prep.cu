@@ -82,6 +82,22 @@ SSM_DEVINL float dot_row(const float *row, const float2 *x) {
     return (a0.x + a0.y) + (a1.x + a1.y);
 }
 
+// The same for two columns x and y at once: a row read from shared memory, whose
+// return bandwidth bounds this kernel, serves both.
+template <int N4>
+SSM_DEVINL float2 dot_row2(const float *row, const float2 *x, const float2 *y) {
+    float2 a = make_float2(0.f, 0.f), b = a;
+#pragma unroll
+    for (int k = 0; k < N4; ++k) {
+        const float4 u = *reinterpret_cast<const float4 *>(row + 4 * k);
+        a = __ffma2_rn(make_float2(u.x, u.y), x[2 * k], a);
+        b = __ffma2_rn(make_float2(u.x, u.y), y[2 * k], b);
+        a = __ffma2_rn(make_float2(u.z, u.w), x[2 * k + 1], a);
+        b = __ffma2_rn(make_float2(u.z, u.w), y[2 * k + 1], b);
+    }
+    return make_float2(a.x + a.y, b.x + b.y);
+}
+
 // T = (I + M)^-1 of one head, in place, then as two bf16 parts, by two warps
 // (`part` 0, 1; they meet at barrier `bar`).  The loops are short on purpose:
 // unrolled altogether they would leave the instruction cache.
@@ -133,19 +149,25 @@ SSM_DEVINL void invert(Head &hd, int lane, int part, int bar) {
         }
     }
     meet();
-    // the 32 x 32 block below: lane = column, 16 rows per warp
-    float2 x[16];
+    // the 32 x 32 block below: 16 rows per warp, 8 per half warp; columns c and c + 16 in each lane
+    float2 x[16], y[16];
+    const auto columns = [&](const float *t) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = make_float2(m[2 * k * kLd + lane], m[(2 * k + 1) * kLd + lane]);
-    const int r0 = 32 + 16 * part;
+        for (int k = 0; k < 16; ++k) {
+            x[k] = make_float2(t[2 * k * kLd + c], t[(2 * k + 1) * kLd + c]);
+            y[k] = make_float2(t[2 * k * kLd + 16 + c], t[(2 * k + 1) * kLd + 16 + c]);
+        }
+    };
+    columns(m);
+    const int r0 = 32 + 16 * part + 8 * up;
 #pragma unroll 1
-    for (int i = r0; i < r0 + 16; i += 4) {
-        float z[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = dot_row<8>(m + (i + e) * kLd, x);
+    for (int i = r0; i < r0 + 8; i += 2) {
+        const float2 z0 = dot_row2<8>(m + i * kLd, x, y), z1 = dot_row2<8>(m + (i + 1) * kLd, x, y);
         __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m[(i + e) * kLd + lane] = z[e];
+        m[i * kLd + c] = z0.x;
+        m[i * kLd + 16 + c] = z0.y;
+        m[(i + 1) * kLd + c] = z1.x;
+        m[(i + 1) * kLd + 16 + c] = z1.y;
     }
     // The high part of T lies over the fp32 rows: row i of it ends at byte 128 (i + 1), row j of those begins at
     // 272 j, so T's rows 0 - 31 (first warp, in order) only meet fp32 rows that are read, and rows 32 - 63 end
@@ -156,9 +178,9 @@ SSM_DEVINL void invert(Head &hd, int lane, int part, int bar) {
         *reinterpret_cast<__nv_bfloat16 *>(hi + swz(i, j)) = h;
         *reinterpret_cast<__nv_bfloat16 *>(lo + swz(i, j)) = __float2bfloat16_rn(v - __bfloat162float(h));
     };
+    if (part == 1 && lane == 0) tc::bulk_wait_read();  // the attention weights have left the low part's place
     meet();                                            // the products are written, T11 is read
-#pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = make_float2(m[(32 + 2 * k) * kLd + lane], m[(33 + 2 * k) * kLd + lane]);
+    columns(m + 32 * kLd);
     if (part == 0)
 #pragma unroll 1
         for (int i = 0; i < 32; i += 4) {
@@ -172,19 +194,39 @@ SSM_DEVINL void invert(Head &hd, int lane, int part, int bar) {
                 put(i + e, 32 + lane, 0.f);
             }
         }
+    else
+        // meanwhile T22, which stays where it is
+#pragma unroll 1
+        for (int i = 32; i < 64; i += 4) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = lane <= i + e - 32 ? m[(i + e) * kLd + 32 + lane] : 0.f;
+            // (high parts of rows 32 - 63 lie over fp32 rows 15 - 30 of T11: after the next meeting)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat16 h = __float2bfloat16_rn(v[e]);
+                *reinterpret_cast<__nv_bfloat16 *>(lo + swz(i + e, 32 + lane)) = __float2bfloat16_rn(v[e] - __bfloat162float(h));
+            }
+        }
     meet();                                            // T11's fp32 rows are read
 #pragma unroll 1
-    for (int i = r0; i < r0 + 16; i += 4) {
-        float z[4], v[4];
+    for (int i = r0; i < r0 + 8; i += 2) {
+        float2 z[2];
+        float v[2][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            z[e] = -dot_row<8>(m + (i + e) * kLd + 32, x);
-            v[e] = lane <= i + e - 32 ? m[(i + e) * kLd + 32 + lane] : 0.f;
+        for (int e = 0; e < 2; ++e) {
+            const float *t = m + (i + e) * kLd + 32;
+            // T22's rows 0 - 15 end at column 16
+            z[e] = part == 0 ? dot_row2<4>(t, x, y) : dot_row2<8>(t, x, y);
+            v[e][0] = t[c];
+            v[e][1] = t[16 + c];
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            put(i + e, lane, z[e]);
-            put(i + e, 32 + lane, v[e]);
+        for (int e = 0; e < 2; ++e) {
+            put(i + e, c, -z[e].x);
+            put(i + e, 16 + c, -z[e].y);
+            *reinterpret_cast<__nv_bfloat16 *>(hi + swz(i + e, 32 + c)) = __float2bfloat16_rn(v[e][0]);
+            *reinterpret_cast<__nv_bfloat16 *>(hi + swz(i + e, 48 + c)) = __float2bfloat16_rn(v[e][1]);
         }
     }
     tc::fence_proxy_async();
@@ -196,7 +238,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
                                                                const __grid_constant__ CUtensorMap tm_k) {
     if (p.err && *p.err != 0) return;
     extern __shared__ uint8_t raw[];
-    PrepSmem &sm = *reinterpret_cast<PrepSmem *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    PrepSmem &sm = *reinterpret_cast<PrepSmem *>(smem_1024(raw));
     const Block b = find_block(p.cu, p.nseqs, p.seqlen, p.nblk, blockIdx.x);
     if (b.nt == 0) return;
     const int h0 = blockIdx.y * p.heads_per_cta, R = p.H / p.G, grp = h0 / R;
@@ -303,16 +345,23 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
                                 const float v1 = j < i ? e1 * (v[e + 2 * f + 1] * p.scale) : 0.f;
                                 split2(v0, v1, o[f], ol[f]);
                             }
-                        uint8_t *at = out + kTBytes + swz(i, 32 * c + e);
-                        *reinterpret_cast<uint4 *>(at) = make_uint4(o[0], o[1], o[2], o[3]);
-                        if (p.bwd) *reinterpret_cast<uint4 *>(at + kTile) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
+                        // by way of T's low part's place: a lane's own row of 128 bytes would take a line per store
+                        *reinterpret_cast<uint4 *>(sm.head[hh].lo + swz(i, 32 * c + e)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (p.bwd)
+                            *reinterpret_cast<uint4 *>(out + kTBytes + kTile + swz(i, 32 * c + e)) =
+                                make_uint4(ol[0], ol[1], ol[2], ol[3]);
                     }
                 }
             }
         }
-        __syncthreads();                               // M is written
+        tc::fence_proxy_async();
+        __syncthreads();                               // M and P are written
         if ((w & 1) < nh) {
             Head &hd = sm.head[w & 1];
+            if (w >= 2 && lane == 0) {
+                bulk_store(p.out + ((int64_t)blockIdx.x * p.H + h0 + hb + w - 2) * hbytes + kTBytes, hd.lo, kTile);
+                asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+            }
             invert(hd, lane, w >> 1, 2 + (w & 1));
             if (tid < 64 && lane == 0) {
                 uint8_t *out = p.out + ((int64_t)blockIdx.x * p.H + h0 + hb + w) * hbytes;

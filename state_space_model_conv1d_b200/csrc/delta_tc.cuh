@@ -41,6 +41,10 @@ struct Rec {
 constexpr float kTinyBeta = 1e-20f;
 SSM_DEVINL float bwd_beta(float b) { return b == 0.f ? kTinyBeta : b; }
 
+// The first 1024-byte boundary of the dynamic shared memory, by an offset: a
+// pointer made from an integer would turn every access into a generic one.
+SSM_DEVINL uint8_t *smem_1024(uint8_t *raw) { return raw + ((0u - tc::smem_u32(raw)) & 1023u); }
+
 // Wait for an mbarrier phase, at most two seconds; gives up as soon as another
 // thread of the CTA has (`abort`), and records the timeout in the error word.
 // The loop is kept out of line: a kernel of many roles waits in dozens of

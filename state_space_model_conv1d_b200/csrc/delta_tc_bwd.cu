@@ -95,7 +95,7 @@ delta_bwd_chain_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, c
     const ssm_delta_args &a = p.b.fwd;
     if (p.sv.err && *p.sv.err != 0) return;
     extern __shared__ uint8_t raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *sm = smem_1024(raw);
     Aux &ax = *reinterpret_cast<Aux *>(sm + L::AUX);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int grp = blockIdx.x / p.units, unit = blockIdx.x % p.units;
@@ -649,7 +649,7 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
     const Block blk = find_block(a.cu_seqlens, p.sv.nseqs, a.seqlen, p.nblk, blockIdx.x);
     if (blk.nt == 0) return;
     extern __shared__ uint8_t raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *sm = smem_1024(raw);
     GradAux &ax = *reinterpret_cast<GradAux *>(sm + L::AUX);
     const uint32_t sb = tc::smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = blockIdx.y;

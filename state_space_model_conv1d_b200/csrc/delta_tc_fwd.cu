@@ -105,7 +105,7 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
     const ssm_delta_args &a = p.a;
     if (p.sv.err && *p.sv.err != 0) return;
     extern __shared__ uint8_t raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *sm = smem_1024(raw);
     Aux &ax = *reinterpret_cast<Aux *>(sm + L::AUX);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
