@@ -149,84 +149,67 @@ SSM_DEVINL void invert(Head &hd, int lane, int part, int bar) {
         }
     }
     meet();
-    // the 32 x 32 block below: 16 rows per warp, 8 per half warp; columns c and c + 16 in each lane
+    // the 32 x 32 block below: 16 rows per warp, 8 per half warp; columns 2 c and 2 c + 1 in each lane
     float2 x[16], y[16];
-    const auto columns = [&](const float *t) {
+    const auto at2 = [&](int row, int col) -> float2 & { return *reinterpret_cast<float2 *>(m + row * kLd + col); };
+    const auto columns = [&](int row) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            x[k] = make_float2(t[2 * k * kLd + c], t[(2 * k + 1) * kLd + c]);
-            y[k] = make_float2(t[2 * k * kLd + 16 + c], t[(2 * k + 1) * kLd + 16 + c]);
+            const float2 u = at2(row + 2 * k, 2 * c), v = at2(row + 2 * k + 1, 2 * c);
+            x[k] = make_float2(u.x, v.x);
+            y[k] = make_float2(u.y, v.y);
         }
     };
-    columns(m);
+    columns(0);
     const int r0 = 32 + 16 * part + 8 * up;
 #pragma unroll 1
     for (int i = r0; i < r0 + 8; i += 2) {
         const float2 z0 = dot_row2<8>(m + i * kLd, x, y), z1 = dot_row2<8>(m + (i + 1) * kLd, x, y);
         __syncwarp();
-        m[i * kLd + c] = z0.x;
-        m[i * kLd + 16 + c] = z0.y;
-        m[(i + 1) * kLd + c] = z1.x;
-        m[(i + 1) * kLd + 16 + c] = z1.y;
+        at2(i, 2 * c) = z0;
+        at2(i + 1, 2 * c) = z1;
     }
     // The high part of T lies over the fp32 rows: row i of it ends at byte 128 (i + 1), row j of those begins at
     // 272 j, so T's rows 0 - 31 (first warp, in order) only meet fp32 rows that are read, and rows 32 - 63 end
     // before fp32 row 32.
     uint8_t *hi = reinterpret_cast<uint8_t *>(m), *lo = hd.lo;
-    const auto put = [&](int i, int j, float v) {
-        const __nv_bfloat16 h = __float2bfloat16_rn(v);
-        *reinterpret_cast<__nv_bfloat16 *>(hi + swz(i, j)) = h;
-        *reinterpret_cast<__nv_bfloat16 *>(lo + swz(i, j)) = __float2bfloat16_rn(v - __bfloat162float(h));
-    };
+    const auto word = [](uint8_t *t, int i, int j) -> uint32_t & { return *reinterpret_cast<uint32_t *>(t + swz(i, j)); };
     if (part == 1 && lane == 0) tc::bulk_wait_read();  // the attention weights have left the low part's place
     meet();                                            // the products are written, T11 is read
-    columns(m + 32 * kLd);
-    if (part == 0)
+    columns(32);
+    const int t0 = 32 * part;                          // first warp: T11; second: T22's low part, T22 itself stays
 #pragma unroll 1
-        for (int i = 0; i < 32; i += 4) {
-            float v[4];
+    for (int i = 0; i < 32; i += 8) {
+        float2 v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = lane <= i + e ? m[(i + e) * kLd + lane] : 0.f;
-            __syncwarp();
+        for (int e = 0; e < 4; ++e) v[e] = at2(t0 + i + 2 * e + up, t0 + 2 * c);
+        __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                put(i + e, lane, v[e]);
-                put(i + e, 32 + lane, 0.f);
+        for (int e = 0; e < 4; ++e) {
+            const int row = i + 2 * e + up;
+            uint32_t h, l;
+            split2(v[e].x, v[e].y, h, l);
+            word(lo, t0 + row, t0 + 2 * c) = l;
+            if (part == 0) {
+                word(hi, row, 2 * c) = h;
+                word(hi, row, 32 + 2 * c) = 0;
+                word(lo, row, 32 + 2 * c) = 0;
             }
         }
-    else
-        // meanwhile T22, which stays where it is
-#pragma unroll 1
-        for (int i = 32; i < 64; i += 4) {
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = lane <= i + e - 32 ? m[(i + e) * kLd + 32 + lane] : 0.f;
-            // (high parts of rows 32 - 63 lie over fp32 rows 15 - 30 of T11: after the next meeting)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat16 h = __float2bfloat16_rn(v[e]);
-                *reinterpret_cast<__nv_bfloat16 *>(lo + swz(i + e, 32 + lane)) = __float2bfloat16_rn(v[e] - __bfloat162float(h));
-            }
-        }
+    }
     meet();                                            // T11's fp32 rows are read
 #pragma unroll 1
     for (int i = r0; i < r0 + 8; i += 2) {
-        float2 z[2];
-        float v[2][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float *t = m + (i + e) * kLd + 32;
             // T22's rows 0 - 15 end at column 16
-            z[e] = part == 0 ? dot_row2<4>(t, x, y) : dot_row2<8>(t, x, y);
-            v[e][0] = t[c];
-            v[e][1] = t[16 + c];
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            put(i + e, c, -z[e].x);
-            put(i + e, 16 + c, -z[e].y);
-            *reinterpret_cast<__nv_bfloat16 *>(hi + swz(i + e, 32 + c)) = __float2bfloat16_rn(v[e][0]);
-            *reinterpret_cast<__nv_bfloat16 *>(hi + swz(i + e, 48 + c)) = __float2bfloat16_rn(v[e][1]);
+            const float *t = m + (i + e) * kLd + 32;
+            const float2 z = part == 0 ? dot_row2<4>(t, x, y) : dot_row2<8>(t, x, y), v = at2(i + e, 32 + 2 * c);
+            uint32_t h, l;
+            split2(-z.x, -z.y, h, l);
+            word(hi, i + e, 2 * c) = h;
+            word(lo, i + e, 2 * c) = l;
+            word(hi, i + e, 32 + 2 * c) = pack2(v.x, v.y);
         }
     }
     tc::fence_proxy_async();
