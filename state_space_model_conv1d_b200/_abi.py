@@ -173,6 +173,9 @@ class PagesArgs(C.Structure):
     ]
 
 
+# These calls take their structure packed into bytes as well as by reference.
+_args = _vp
+
 SIGNATURES = {
     "ssm_abi_version": ([], _i32),
     "ssm_status_string": ([_i32], C.c_char_p),
@@ -192,19 +195,19 @@ SIGNATURES = {
     "ssm_split_cum_delta": ([C.POINTER(ScanArgs), _vp, _vp, _vp], _i32),
     "ssm_split_combine": ([C.POINTER(SplitArgs), _vp], _i32),
     "ssm_split_fixup": ([C.POINTER(ScanArgs), _vp, _vp, _vp], _i32),
-    "ssm_delta_workspace_size": ([C.POINTER(DeltaArgs)], C.c_size_t),
-    "ssm_delta_fwd": ([C.POINTER(DeltaArgs), _vp, C.c_size_t, _vp], _i32),
-    "ssm_delta_bwd_workspace_size": ([C.POINTER(DeltaBwdArgs)], C.c_size_t),
-    "ssm_delta_bwd": ([C.POINTER(DeltaBwdArgs), _vp, C.c_size_t, _vp], _i32),
-    "ssm_delta_update": ([C.POINTER(DeltaUpdateArgs), _vp], _i32),
-    "ssm_group_norm_fwd": ([C.POINTER(NormArgs), _vp], _i32),
-    "ssm_group_norm_bwd_workspace_size": ([C.POINTER(NormBwdArgs)], C.c_size_t),
-    "ssm_group_norm_bwd": ([C.POINTER(NormBwdArgs), _vp, C.c_size_t, _vp], _i32),
-    "ssm_pages_workspace_size": ([C.POINTER(PagesArgs)], C.c_size_t),
-    "ssm_pages_copy": ([C.POINTER(PagesArgs), _vp, C.c_size_t, _vp], _i32),
-    "ssm_pages_fork": ([C.POINTER(PagesArgs), _vp, C.c_size_t, _vp], _i32),
-    "ssm_pages_free": ([C.POINTER(PagesArgs), _vp, C.c_size_t, _vp], _i32),
-    "ssm_pages_compact": ([C.POINTER(PagesArgs), _vp, C.c_size_t, _vp], _i32),
+    "ssm_delta_workspace_size": ([_args], C.c_size_t),
+    "ssm_delta_fwd": ([_args, _vp, C.c_size_t, _vp], _i32),
+    "ssm_delta_bwd_workspace_size": ([_args], C.c_size_t),
+    "ssm_delta_bwd": ([_args, _vp, C.c_size_t, _vp], _i32),
+    "ssm_delta_update": ([_args, _vp], _i32),
+    "ssm_group_norm_fwd": ([_args, _vp], _i32),
+    "ssm_group_norm_bwd_workspace_size": ([_args], C.c_size_t),
+    "ssm_group_norm_bwd": ([_args, _vp, C.c_size_t, _vp], _i32),
+    "ssm_pages_workspace_size": ([_args], C.c_size_t),
+    "ssm_pages_copy": ([_args, _vp, C.c_size_t, _vp], _i32),
+    "ssm_pages_fork": ([_args, _vp, C.c_size_t, _vp], _i32),
+    "ssm_pages_free": ([_args, _vp, C.c_size_t, _vp], _i32),
+    "ssm_pages_compact": ([_args, _vp, C.c_size_t, _vp], _i32),
     "ssm_check_bounds_enabled": ([], _i32),
     "ssm_bounds_record": ([C.POINTER(_i32), C.POINTER(_i32), C.POINTER(_i64), C.POINTER(_i64), _i32], _i32),
 }
