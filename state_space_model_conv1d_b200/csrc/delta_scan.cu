@@ -129,11 +129,21 @@ __global__ void __launch_bounds__(threads_of<W>()) delta_scan_kernel(const Args 
     const int r = warp * 4 + (lane >> 3);              // row within the CTA
     const bool live = p0 + r < P;
     const int64_t srow = ((int64_t)sq.s * H + h) * P + p0 + r;
-    float st[NE];
-    if (live && a.h0) load_row<NE>(st, a.h0 + srow * N, lane8, N);
-    else
+    float2 st2[NE / 2];
+    {
+        float st[NE];
+        if (live && a.h0) load_row<NE>(st, a.h0 + srow * N, lane8, N);
+        else
 #pragma unroll
-        for (int e = 0; e < NE; ++e) st[e] = 0.f;
+            for (int e = 0; e < NE; ++e) st[e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < NE / 2; ++e) st2[e] = make_float2(st[2 * e], st[2 * e + 1]);
+    }
+    const auto keep = [&](float *o) {
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+            if (state_of(lane8, e) < N) o[state_of(lane8, e)] = e & 1 ? st2[e / 2].y : st2[e / 2].x;
+    };
 
     const T *q = (const T *)a.q + sq.row * a.q_batch_stride + grp * N;
     const T *k = (const T *)a.k + sq.row * a.k_batch_stride + grp * N;
@@ -158,12 +168,8 @@ __global__ void __launch_bounds__(threads_of<W>()) delta_scan_kernel(const Args 
     if (sq.lo < sq.hi) fetch(sq.lo);
     for (int64_t t0 = sq.lo; t0 < sq.hi; t0 += kTok) {
         const int nt = (int)min((int64_t)kTok, sq.hi - t0);
-        if (p.ckpt && live && (t0 - sq.lo) % kDeltaCkpt == 0) {
-            float *c = p.ckpt + (((sq.ckpt_row + (t0 - sq.lo) / kDeltaCkpt) * H + h) * P + p0 + r) * N;
-#pragma unroll
-            for (int e = 0; e < NE; ++e)
-                if (state_of(lane8, e) < N) c[state_of(lane8, e)] = st[e];
-        }
+        if (p.ckpt && live && (t0 - sq.lo) % kDeltaCkpt == 0)
+            keep(p.ckpt + (((sq.ckpt_row + (t0 - sq.lo) / kDeltaCkpt) * H + h) * P + p0 + r) * N);
         __syncthreads();                               // the tokens before are read
         sk_.store(ks);
         if (y) sq_s.store(qs);
@@ -175,47 +181,41 @@ __global__ void __launch_bounds__(threads_of<W>()) delta_scan_kernel(const Args 
         __syncthreads();
         if (t0 + kTok < sq.hi) fetch(t0 + kTok);
         for (int t = 0; t < nt; ++t) {
-            const float al = as[t];
-            float sk2[2] = {0.f, 0.f}, sq2[2] = {0.f, 0.f}, kq = 0.f, kk[NE];        // two chains a sum
+            // packed pairs of states, two chains a sum
+            const float2 al = make_float2(as[t], as[t]), zero = make_float2(0.f, 0.f);
+            float2 sk2[2] = {zero, zero}, sq2[2] = {zero, zero}, kq2[2] = {zero, zero}, kk[NE / 2];
 #pragma unroll
-            for (int e = 0; e < NE; e += 4) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(ks + t * NP + state_of(lane8, e));
-                kk[e] = k4.x; kk[e + 1] = k4.y; kk[e + 2] = k4.z; kk[e + 3] = k4.w;
+            for (int e = 0; e < NE / 4; ++e) {
+                const float4 k4 = *reinterpret_cast<const float4 *>(ks + t * NP + state_of(lane8, 4 * e));
+                kk[2 * e] = make_float2(k4.x, k4.y);
+                kk[2 * e + 1] = make_float2(k4.z, k4.w);
             }
 #pragma unroll
-            for (int e = 0; e < NE; ++e) {
-                st[e] *= al;
-                sk2[e & 1] = fmaf(st[e], kk[e], sk2[e & 1]);
+            for (int e = 0; e < NE / 2; ++e) {
+                st2[e] = __fmul2_rn(st2[e], al);
+                sk2[e & 1] = __ffma2_rn(st2[e], kk[e], sk2[e & 1]);
             }
             if (y) {
 #pragma unroll
-                for (int e = 0; e < NE; e += 4) {
-                    const float4 q4 = *reinterpret_cast<const float4 *>(qs + t * NP + state_of(lane8, e));
-                    sq2[0] = fmaf(st[e], q4.x, sq2[0]);
-                    sq2[1] = fmaf(st[e + 1], q4.y, sq2[1]);
-                    sq2[0] = fmaf(st[e + 2], q4.z, sq2[0]);
-                    sq2[1] = fmaf(st[e + 3], q4.w, sq2[1]);
-                    kq = fmaf(kk[e], q4.x, kq);
-                    kq = fmaf(kk[e + 1], q4.y, kq);
-                    kq = fmaf(kk[e + 2], q4.z, kq);
-                    kq = fmaf(kk[e + 3], q4.w, kq);
+                for (int e = 0; e < NE / 4; ++e) {
+                    const float4 q4 = *reinterpret_cast<const float4 *>(qs + t * NP + state_of(lane8, 4 * e));
+                    const float2 qa = make_float2(q4.x, q4.y), qb = make_float2(q4.z, q4.w);
+                    sq2[0] = __ffma2_rn(st2[2 * e], qa, sq2[0]);
+                    sq2[1] = __ffma2_rn(st2[2 * e + 1], qb, sq2[1]);
+                    kq2[0] = __ffma2_rn(kk[2 * e], qa, kq2[0]);
+                    kq2[1] = __ffma2_rn(kk[2 * e + 1], qb, kq2[1]);
                 }
             }
-            const float sk = sum8(sk2[0] + sk2[1]), sq_ = y ? sum8(sq2[0] + sq2[1]) : 0.f;
-            if (y) kq = sum8(kq);
+            const auto sum = [](const float2(&x)[2]) { return sum8((x[0].x + x[0].y) + (x[1].x + x[1].y)); };
+            const float sk = sum(sk2), sq_ = y ? sum(sq2) : 0.f, kq = y ? sum(kq2) : 0.f;
             const float u = bs[t] * (vs[t * kRows + r] - sk);
 #pragma unroll
-            for (int e = 0; e < NE; ++e) st[e] = fmaf(u, kk[e], st[e]);
+            for (int e = 0; e < NE / 2; ++e) st2[e] = __ffma2_rn(make_float2(u, u), kk[e], st2[e]);
             if (y && lane8 == 0 && live)
                 Elem<T>::st(y + (t0 + t) * a.y_token_stride + r, a.scale * fmaf(u, kq, sq_));
         }
     }
-    if (a.h_final && live) {
-        float *o = a.h_final + srow * N;
-#pragma unroll
-        for (int e = 0; e < NE; ++e)
-            if (state_of(lane8, e) < N) o[state_of(lane8, e)] = st[e];
-    }
+    if (a.h_final && live) keep(a.h_final + srow * N);
 }
 
 // ------------------------------------------------------------------ backward
