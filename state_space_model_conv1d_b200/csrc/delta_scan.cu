@@ -5,18 +5,17 @@
 //     w = a_t h,  s = w . k_t,  u = beta_t (v_t[p] - s),  h = w + u k_t,
 //     y_t[p] = scale (h . q_t) = scale (w . q_t + u (k_t . q_t)),
 // so rows are spread over lanes: 8 lanes hold one row (4 consecutive states
-// of every 32), a warp holds 4 rows.  The two dot products of a token are
-// summed in one pass of 3 shuffle levels.  The chain over the tokens bounds
-// the time (about 100 ns a token: two FMA chains, the shuffles, one row of
-// shared memory), not memory; a sequence's rows run in separate CTAs.
+// of every 32) and a warp 4 rows, or a warp one row.  The dot products of a
+// token are summed in one pass of shuffles.  The chain over the tokens bounds
+// the time, not memory; a sequence's rows run in separate CTAs.
 //
 // Backward, per row, from the last token to the first, with d = dL/dh_t:
 //     d += scale dy q;  du = d . k;  dv = beta du;  ds = -beta du;
 //     dbeta = sum_p du (v - s);  dq = scale sum_p dy h_t;
 //     dk = sum_p (u d + ds w);  d += ds k;  dg = sum_{p,n} d w;  d = a d.
 // The states before every 32nd token are kept by a forward pass; the tokens
-// between are recomputed in runs that fit in registers.  Each CTA owns 32 rows
-// and writes their share of dq, dk, dg, dbeta; a second kernel adds the shares
+// between are recomputed in runs that fit in registers.  Each CTA owns some
+// rows and writes their share of dq, dk, dg, dbeta; a second kernel adds the shares
 // in a fixed order.
 #include "common.cuh"
 #include "delta.h"
@@ -24,12 +23,13 @@
 namespace ssm {
 namespace {
 
-// W warps per CTA: 8 (32 state rows), or 2 (8 rows) where CTAs of 8 would leave
-// SMs idle; a token's row of k and q is read from shared memory by every warp,
-// and with 8 warps on one SM that bounds the token (2 x 333 tokens, 6 heads,
-// P 40, N 72: 166 us with 8, 75 us with 2).
-template <int W> constexpr int threads_of() { return W * 32; }
-template <int W> constexpr int rows_of() { return W * 4; }
+// L lanes per state row and W warps per CTA: 8 and 8 (32 rows per CTA), or, where
+// that gives a scheduler less than a warp, 32 and 4 (4 rows): the chain over the
+// tokens is latency, and a quarter of the states per lane is a third of the
+// instructions of a token.
+template <int L, int W> struct Cut {
+    static constexpr int threads = W * 32, rows = W * 32 / L, per_warp = 32 / L;
+};
 
 struct Args {
     ssm_delta_args a;
@@ -60,8 +60,8 @@ SSM_DEVINL Seq find_seq(const ssm_delta_args &a, const SeqView &sv, int y) {
     return q;
 }
 
-// State index of element e of this lane: 4 consecutive of every 32.
-SSM_DEVINL int state_of(int lane8, int e) { return (e >> 2) * 32 + lane8 * 4 + (e & 3); }
+// State index of element e of a row's lane: 4 consecutive of every 4 L.
+template <int L> SSM_DEVINL int state_of(int lrow, int e) { return (e >> 2) * 4 * L + lrow * 4 + (e & 3); }
 
 // `nt` tokens of a [tokens][width] operand on the way to shared memory, fp32,
 // PAD columns wide (zeros past width and behind nt): all of a thread's loads
@@ -95,29 +95,27 @@ template <typename T, int PAD, int kTok, int kThreads> struct Staged {
 };
 SSM_DEVINL float decay_of(float g) { return expf(fmaxf(g, kMinLogDecay)); }
 
-template <int NE>
-SSM_DEVINL void load_row(float (&h)[NE], const float *src, int lane8, int64_t N) {
+template <int NE, int L>
+SSM_DEVINL void load_row(float (&h)[NE], const float *src, int lrow, int64_t N) {
 #pragma unroll
     for (int e = 0; e < NE; ++e) {
-        const int n = state_of(lane8, e);
+        const int n = state_of<L>(lrow, e);
         h[e] = n < N ? src[n] : 0.f;
     }
 }
-SSM_DEVINL float sum8(float v) {
-    v += __shfl_xor_sync(~0u, v, 1);
-    v += __shfl_xor_sync(~0u, v, 2);
-    v += __shfl_xor_sync(~0u, v, 4);
+// Sum over a row's lanes.
+template <int L> SSM_DEVINL float row_sum(float v) {
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) v += __shfl_xor_sync(~0u, v, o);
     return v;
 }
 
-template <int W> constexpr int fwd_tokens() { return W == 8 ? 32 : 8; }    // tokens staged at a time
-
-template <typename T, int NE, int W>
-__global__ void __launch_bounds__(threads_of<W>()) delta_scan_kernel(const Args p) {
-    constexpr int kThreads = threads_of<W>(), kRows = rows_of<W>(), kTok = fwd_tokens<W>();
+template <typename T, int NE, int L, int W>
+__global__ void __launch_bounds__(W * 32) delta_scan_kernel(const Args p) {
+    constexpr int kThreads = Cut<L, W>::threads, kRows = Cut<L, W>::rows, kTok = kDeltaCkpt;   // tokens staged at a time
     const ssm_delta_args &a = p.a;
     if (p.sv.err && *p.sv.err != 0) return;
-    constexpr int NP = NE * 8;
+    constexpr int NP = NE * L;
     extern __shared__ float sm[];
     float *ks = sm, *qs = ks + kTok * NP, *vs = qs + kTok * NP, *as = vs + kTok * kRows, *bs = as + kTok;
     const Seq sq = find_seq(a, p.sv, blockIdx.y);
@@ -125,14 +123,14 @@ __global__ void __launch_bounds__(threads_of<W>()) delta_scan_kernel(const Args 
     const int h = blockIdx.x % H, p0 = (int)(blockIdx.x / H) * kRows;
     const int grp = (int)(h / (H / a.ngroups));
     if (!SSM_BOUNDS(sq.hi, a.seqlen + 1, BS_DELTA_SEQ) || !SSM_BOUNDS(sq.lo, sq.hi + 1, BS_DELTA_SEQ)) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lane8 = lane & 7;
-    const int r = warp * 4 + (lane >> 3);              // row within the CTA
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lrow = lane % L;
+    const int r = warp * Cut<L, W>::per_warp + lane / L;       // row within the CTA
     const bool live = p0 + r < P;
     const int64_t srow = ((int64_t)sq.s * H + h) * P + p0 + r;
     float2 st2[NE / 2];
     {
         float st[NE];
-        if (live && a.h0) load_row<NE>(st, a.h0 + srow * N, lane8, N);
+        if (live && a.h0) load_row<NE, L>(st, a.h0 + srow * N, lrow, N);
         else
 #pragma unroll
             for (int e = 0; e < NE; ++e) st[e] = 0.f;
@@ -142,7 +140,7 @@ __global__ void __launch_bounds__(threads_of<W>()) delta_scan_kernel(const Args 
     const auto keep = [&](float *o) {
 #pragma unroll
         for (int e = 0; e < NE; ++e)
-            if (state_of(lane8, e) < N) o[state_of(lane8, e)] = e & 1 ? st2[e / 2].y : st2[e / 2].x;
+            if (state_of<L>(lrow, e) < N) o[state_of<L>(lrow, e)] = e & 1 ? st2[e / 2].y : st2[e / 2].x;
     };
 
     const T *q = (const T *)a.q + sq.row * a.q_batch_stride + grp * N;
@@ -168,7 +166,7 @@ __global__ void __launch_bounds__(threads_of<W>()) delta_scan_kernel(const Args 
     if (sq.lo < sq.hi) fetch(sq.lo);
     for (int64_t t0 = sq.lo; t0 < sq.hi; t0 += kTok) {
         const int nt = (int)min((int64_t)kTok, sq.hi - t0);
-        if (p.ckpt && live && (t0 - sq.lo) % kDeltaCkpt == 0)
+        if (p.ckpt && live)
             keep(p.ckpt + (((sq.ckpt_row + (t0 - sq.lo) / kDeltaCkpt) * H + h) * P + p0 + r) * N);
         __syncthreads();                               // the tokens before are read
         sk_.store(ks);
@@ -186,7 +184,7 @@ __global__ void __launch_bounds__(threads_of<W>()) delta_scan_kernel(const Args 
             float2 sk2[2] = {zero, zero}, sq2[2] = {zero, zero}, kq2[2] = {zero, zero}, kk[NE / 2];
 #pragma unroll
             for (int e = 0; e < NE / 4; ++e) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(ks + t * NP + state_of(lane8, 4 * e));
+                const float4 k4 = *reinterpret_cast<const float4 *>(ks + t * NP + state_of<L>(lrow, 4 * e));
                 kk[2 * e] = make_float2(k4.x, k4.y);
                 kk[2 * e + 1] = make_float2(k4.z, k4.w);
             }
@@ -198,7 +196,7 @@ __global__ void __launch_bounds__(threads_of<W>()) delta_scan_kernel(const Args 
             if (y) {
 #pragma unroll
                 for (int e = 0; e < NE / 4; ++e) {
-                    const float4 q4 = *reinterpret_cast<const float4 *>(qs + t * NP + state_of(lane8, 4 * e));
+                    const float4 q4 = *reinterpret_cast<const float4 *>(qs + t * NP + state_of<L>(lrow, 4 * e));
                     const float2 qa = make_float2(q4.x, q4.y), qb = make_float2(q4.z, q4.w);
                     sq2[0] = __ffma2_rn(st2[2 * e], qa, sq2[0]);
                     sq2[1] = __ffma2_rn(st2[2 * e + 1], qb, sq2[1]);
@@ -206,12 +204,12 @@ __global__ void __launch_bounds__(threads_of<W>()) delta_scan_kernel(const Args 
                     kq2[1] = __ffma2_rn(kk[2 * e + 1], qb, kq2[1]);
                 }
             }
-            const auto sum = [](const float2(&x)[2]) { return sum8((x[0].x + x[0].y) + (x[1].x + x[1].y)); };
+            const auto sum = [](const float2(&x)[2]) { return row_sum<L>((x[0].x + x[0].y) + (x[1].x + x[1].y)); };
             const float sk = sum(sk2), sq_ = y ? sum(sq2) : 0.f, kq = y ? sum(kq2) : 0.f;
             const float u = bs[t] * (vs[t * kRows + r] - sk);
 #pragma unroll
             for (int e = 0; e < NE / 2; ++e) st2[e] = __ffma2_rn(make_float2(u, u), kk[e], st2[e]);
-            if (y && lane8 == 0 && live)
+            if (y && lrow == 0 && live)
                 Elem<T>::st(y + (t0 + t) * a.y_token_stride + r, a.scale * fmaf(u, kq, sq_));
         }
     }
@@ -227,31 +225,41 @@ struct BwdArgs {
     float *pg, *pb;        // [slices][tokens][H]
 };
 
-// Sum over the 4 rows of a warp; lane group i (lanes 8i .. 8i+7) ends with a
-// quarter of the elements, NE / 4 of them: elements i * NE/4 ...
-template <int NE>
-SSM_DEVINL void rows_sum(float (&x)[NE], float (&out)[NE / 4], int lane) {
-    const bool hi = lane & 16, hi2 = lane & 8;
-    float y[NE / 2];
+// Sum over the rows of a warp.  With 4 rows lane group i (lanes 8 i .. 8 i + 7)
+// ends with a quarter of the elements, those from first_of() on; with one row
+// there is nothing to add.
+template <int NE, int L> constexpr int kept() { return L == 32 ? NE : NE / 4; }
+template <int NE, int L> SSM_DEVINL int first_of(int lane) {
+    return L == 32 ? 0 : (((lane >> 4) & 1) * 2 + ((lane >> 3) & 1)) * (NE / 4);
+}
+template <int NE, int L>
+SSM_DEVINL void rows_sum(float (&x)[NE], float (&out)[kept<NE, L>()], int lane) {
+    if constexpr (L == 32) {
 #pragma unroll
-    for (int e = 0; e < NE / 2; ++e) {
-        const float give = hi ? x[e] : x[e + NE / 2], keep = hi ? x[e + NE / 2] : x[e];
-        y[e] = keep + __shfl_xor_sync(~0u, give, 16);
-    }
+        for (int e = 0; e < NE; ++e) out[e] = x[e];
+    } else {
+        const bool hi = lane & 16, hi2 = lane & 8;
+        float y[NE / 2];
 #pragma unroll
-    for (int e = 0; e < NE / 4; ++e) {
-        const float give = hi2 ? y[e] : y[e + NE / 4], keep = hi2 ? y[e + NE / 4] : y[e];
-        out[e] = keep + __shfl_xor_sync(~0u, give, 8);
+        for (int e = 0; e < NE / 2; ++e) {
+            const float give = hi ? x[e] : x[e + NE / 2], keep = hi ? x[e + NE / 2] : x[e];
+            y[e] = keep + __shfl_xor_sync(~0u, give, 16);
+        }
+#pragma unroll
+        for (int e = 0; e < NE / 4; ++e) {
+            const float give = hi2 ? y[e] : y[e + NE / 4], keep = hi2 ? y[e + NE / 4] : y[e];
+            out[e] = keep + __shfl_xor_sync(~0u, give, 8);
+        }
     }
 }
 
 // TR tokens are held in registers at a time (TR * NE states each).
-template <typename T, int NE, int TR, int W>
-__global__ void __launch_bounds__(threads_of<W>(), 1) delta_scan_bwd_kernel(const BwdArgs p) {
-    constexpr int kThreads = threads_of<W>(), kRows = rows_of<W>(), kTok = kDeltaCkpt, kWarps = W;
+template <typename T, int NE, int TR, int L, int W>
+__global__ void __launch_bounds__(W * 32, 1) delta_scan_bwd_kernel(const BwdArgs p) {
+    constexpr int kThreads = Cut<L, W>::threads, kRows = Cut<L, W>::rows, kTok = kDeltaCkpt, kWarps = W;
     const ssm_delta_args &a = p.b.fwd;
     if (p.sv.err && *p.sv.err != 0) return;
-    constexpr int NP = NE * 8;
+    constexpr int NP = NE * L;
     extern __shared__ float sm[];
     float *ks = sm, *qs = ks + kTok * NP, *vs = qs + kTok * NP, *ds_ = vs + kTok * kRows, *as = ds_ + kTok * kRows,
           *bs = as + kTok;
@@ -264,12 +272,12 @@ __global__ void __launch_bounds__(threads_of<W>(), 1) delta_scan_bwd_kernel(cons
     const int h = blockIdx.x % H, slice = (int)(blockIdx.x / H), p0 = slice * kRows;
     const int grp = (int)(h / (H / a.ngroups));
     if (!SSM_BOUNDS(sq.hi, a.seqlen + 1, BS_DELTA_SEQ) || !SSM_BOUNDS(sq.lo, sq.hi + 1, BS_DELTA_SEQ)) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lane8 = lane & 7;
-    const int r = warp * 4 + (lane >> 3);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lrow = lane % L;
+    const int r = warp * Cut<L, W>::per_warp + lane / L;
     const bool live = p0 + r < P;
     const int64_t srow = ((int64_t)sq.s * H + h) * P + p0 + r;
     float d[NE];
-    if (live && p.b.dh_final) load_row<NE>(d, p.b.dh_final + srow * N, lane8, N);
+    if (live && p.b.dh_final) load_row<NE, L>(d, p.b.dh_final + srow * N, lrow, N);
     else
 #pragma unroll
         for (int e = 0; e < NE; ++e) d[e] = 0.f;
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(threads_of<W>(), 1) delta_scan_bwd_kernel(cons
         const float *cp = p.ckpt + (((sq.ckpt_row + c) * H + h) * P + p0 + r) * N;
         for (int run = (nt + TR - 1) / TR - 1; run >= 0; --run) {
             float st[NE];
-            if (live) load_row<NE>(st, cp, lane8, N);
+            if (live) load_row<NE, L>(st, cp, lrow, N);
             else
 #pragma unroll
                 for (int e = 0; e < NE; ++e) st[e] = 0.f;
@@ -319,11 +327,11 @@ __global__ void __launch_bounds__(threads_of<W>(), 1) delta_scan_bwd_kernel(cons
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
                     st[e] *= as[t];
-                    sk = fmaf(st[e], ks[t * NP + state_of(lane8, e)], sk);
+                    sk = fmaf(st[e], ks[t * NP + state_of<L>(lrow, e)], sk);
                 }
-                const float u = bs[t] * (vs[t * kRows + r] - sum8(sk));
+                const float u = bs[t] * (vs[t * kRows + r] - row_sum<L>(sk));
 #pragma unroll
-                for (int e = 0; e < NE; ++e) st[e] = fmaf(u, ks[t * NP + state_of(lane8, e)], st[e]);
+                for (int e = 0; e < NE; ++e) st[e] = fmaf(u, ks[t * NP + state_of<L>(lrow, e)], st[e]);
             }
             // through the run: w = a h_{t-1} of every token stays in registers
             float w[TR][NE], uu[TR], sk_[TR];
@@ -334,45 +342,44 @@ __global__ void __launch_bounds__(threads_of<W>(), 1) delta_scan_bwd_kernel(cons
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
                     w[i][e] = st[e] * as[t];
-                    sk = fmaf(w[i][e], ks[t * NP + state_of(lane8, e)], sk);
+                    sk = fmaf(w[i][e], ks[t * NP + state_of<L>(lrow, e)], sk);
                 }
-                sk_[i] = sum8(sk);
+                sk_[i] = row_sum<L>(sk);
                 uu[i] = bs[t] * (vs[t * kRows + r] - sk_[i]);
 #pragma unroll
-                for (int e = 0; e < NE; ++e) st[e] = fmaf(uu[i], ks[t * NP + state_of(lane8, e)], w[i][e]);
+                for (int e = 0; e < NE; ++e) st[e] = fmaf(uu[i], ks[t * NP + state_of<L>(lrow, e)], w[i][e]);
             }
 #pragma unroll
             for (int i = TR - 1; i >= 0; --i) {
                 const int t = run * TR + i;
                 const float dyv = a.scale * ds_[t * kRows + r];
-                float x[NE], part[NE / 4], du = 0.f;
+                float x[NE], part[kept<NE, L>()], du = 0.f;
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
-                    const int n = t * NP + state_of(lane8, e);
+                    const int n = t * NP + state_of<L>(lrow, e);
                     x[e] = dyv * fmaf(uu[i], ks[n], w[i][e]);          // dq: dy h_t
                     d[e] = fmaf(dyv, qs[n], d[e]);
                     du = fmaf(d[e], ks[n], du);
                 }
-                du = sum8(du);
-                rows_sum<NE>(x, part, lane);
-                // lanes 8i .. 8i+7 hold elements of quarter ((lane>>4)&1)*2 + ((lane>>3)&1)
-                const int q4 = ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1);
+                du = row_sum<L>(du);
+                rows_sum<NE, L>(x, part, lane);
+                const int e0 = first_of<NE, L>(lane);
 #pragma unroll
-                for (int e = 0; e < NE / 4; ++e) rq[(i * kWarps + warp) * NP + state_of(lane8, q4 * (NE / 4) + e)] = part[e];
+                for (int e = 0; e < kept<NE, L>(); ++e) rq[(i * kWarps + warp) * NP + state_of<L>(lrow, e0 + e)] = part[e];
                 const float dsv = -bs[t] * du;
                 float dg = 0.f;
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
-                    const int n = t * NP + state_of(lane8, e);
+                    const int n = t * NP + state_of<L>(lrow, e);
                     x[e] = fmaf(uu[i], d[e], dsv * w[i][e]);
                     d[e] = fmaf(dsv, ks[n], d[e]);
                     dg = fmaf(d[e], w[i][e], dg);
                     d[e] *= as[t];
                 }
-                rows_sum<NE>(x, part, lane);
+                rows_sum<NE, L>(x, part, lane);
 #pragma unroll
-                for (int e = 0; e < NE / 4; ++e) rk[(i * kWarps + warp) * NP + state_of(lane8, q4 * (NE / 4) + e)] = part[e];
-                float db = lane8 == 0 ? du * (vs[t * kRows + r] - sk_[i]) : 0.f;
+                for (int e = 0; e < kept<NE, L>(); ++e) rk[(i * kWarps + warp) * NP + state_of<L>(lrow, e0 + e)] = part[e];
+                float db = lrow == 0 ? du * (vs[t * kRows + r] - sk_[i]) : 0.f;
 #pragma unroll
                 for (int o = 16; o; o >>= 1) {
                     dg += __shfl_xor_sync(~0u, dg, o);
@@ -382,7 +389,7 @@ __global__ void __launch_bounds__(threads_of<W>(), 1) delta_scan_bwd_kernel(cons
                     rg[i * kWarps + warp] = dg;
                     rb[i * kWarps + warp] = db;
                 }
-                if (lane8 == 0 && live && t < nt)
+                if (lrow == 0 && live && t < nt)
                     Elem<T>::st(dv + (tok0 + t0 + t) * H * P + r, -dsv);
             }
             __syncthreads();
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(threads_of<W>(), 1) delta_scan_bwd_kernel(cons
         float *o = p.b.dh0 + srow * N;
 #pragma unroll
         for (int e = 0; e < NE; ++e)
-            if (state_of(lane8, e) < N) o[state_of(lane8, e)] = d[e];
+            if (state_of<L>(lrow, e) < N) o[state_of<L>(lrow, e)] = d[e];
     }
 }
 
@@ -457,47 +464,53 @@ cudaError_t set_smem(K kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, int NE, int W>
+template <typename T, int NE, int L, int W>
 cudaError_t run_fwd(const Args &p, cudaStream_t st) {
-    constexpr int kTok = fwd_tokens<W>();
+    constexpr int kTok = kDeltaCkpt, kRows = Cut<L, W>::rows;
     const ssm_delta_args &a = p.a;
-    const dim3 grid((unsigned)(a.nheads * ((a.headdim + rows_of<W>() - 1) / rows_of<W>())),
-                    (unsigned)(a.cu_seqlens ? a.nseqs : a.batch));
-    const size_t smem = (size_t)(2 * kTok * NE * 8 + kTok * rows_of<W>() + 2 * kTok) * 4;
-    cudaError_t e = set_smem(delta_scan_kernel<T, NE, W>, smem);
+    const dim3 grid((unsigned)(a.nheads * ((a.headdim + kRows - 1) / kRows)), (unsigned)(a.cu_seqlens ? a.nseqs : a.batch));
+    const size_t smem = (size_t)(2 * kTok * NE * L + kTok * kRows + 2 * kTok) * 4;
+    cudaError_t e = set_smem(delta_scan_kernel<T, NE, L, W>, smem);
     if (e != cudaSuccess) return e;
-    delta_scan_kernel<T, NE, W><<<grid, threads_of<W>(), smem, st>>>(p);
+    delta_scan_kernel<T, NE, L, W><<<grid, W * 32, smem, st>>>(p);
     return cudaGetLastError();
 }
-template <typename T, int NE, int TR, int W>
+template <typename T, int NE, int TR, int L, int W>
 cudaError_t run_bwd(const BwdArgs &p, cudaStream_t st) {
-    constexpr int kTok = kDeltaCkpt;
+    constexpr int kTok = kDeltaCkpt, kRows = Cut<L, W>::rows;
     const ssm_delta_args &a = p.b.fwd;
-    const dim3 grid((unsigned)(a.nheads * ((a.headdim + rows_of<W>() - 1) / rows_of<W>())),
-                    (unsigned)(a.cu_seqlens ? a.nseqs : a.batch));
-    const size_t smem =
-        (size_t)(2 * kTok * NE * 8 + 2 * kTok * rows_of<W>() + 2 * kTok + 2 * TR * W * NE * 8 + 2 * TR * W) * 4;
-    cudaError_t e = set_smem(delta_scan_bwd_kernel<T, NE, TR, W>, smem);
+    const dim3 grid((unsigned)(a.nheads * ((a.headdim + kRows - 1) / kRows)), (unsigned)(a.cu_seqlens ? a.nseqs : a.batch));
+    const size_t smem = (size_t)(2 * kTok * NE * L + 2 * kTok * kRows + 2 * kTok + 2 * TR * W * NE * L + 2 * TR * W) * 4;
+    cudaError_t e = set_smem(delta_scan_bwd_kernel<T, NE, TR, L, W>, smem);
     if (e != cudaSuccess) return e;
-    delta_scan_bwd_kernel<T, NE, TR, W><<<grid, threads_of<W>(), smem, st>>>(p);
+    delta_scan_bwd_kernel<T, NE, TR, L, W><<<grid, W * 32, smem, st>>>(p);
     return cudaGetLastError();
-}
-template <typename T, int NE>
-cudaError_t pick_fwd(const Args &p, int w, cudaStream_t st) {
-    return w == 8 ? run_fwd<T, NE, 8>(p, st) : run_fwd<T, NE, 2>(p, st);
-}
-template <typename T, int NE, int TR>
-cudaError_t pick_bwd(const BwdArgs &p, int w, cudaStream_t st) {
-    return w == 8 ? run_bwd<T, NE, TR, 8>(p, st) : run_bwd<T, NE, TR, 2>(p, st);
 }
 
 int64_t seqs_of(const ssm_delta_args &a) { return a.cu_seqlens ? a.nseqs : a.batch; }
-int warps_of(const ssm_delta_args &a) {
-    return seqs_of(a) * a.nheads * ((a.headdim + rows_of<8>() - 1) / rows_of<8>()) < sm_count() ? 2 : 8;
-}
+// Few rows: with 4 of them a warp, less than a warp for each of the GPU's schedulers.
+bool few_rows(const ssm_delta_args &a) { return seqs_of(a) * a.nheads * a.headdim < 4LL * 4 * sm_count(); }
 int64_t slices_of(const ssm_delta_args &a) {
-    const int rows = warps_of(a) * 4;
+    const int rows = few_rows(a) ? Cut<32, 4>::rows : Cut<8, 8>::rows;
     return (a.headdim + rows - 1) / rows;
+}
+template <typename T>
+cudaError_t pick_fwd(const Args &p, cudaStream_t st) {
+    const int64_t N = p.a.dstate;
+    if (few_rows(p.a)) return N <= 128 ? run_fwd<T, 4, 32, 4>(p, st) : run_fwd<T, 8, 32, 4>(p, st);
+    if (N <= 32) return run_fwd<T, 4, 8, 8>(p, st);
+    if (N <= 64) return run_fwd<T, 8, 8, 8>(p, st);
+    if (N <= 96) return run_fwd<T, 12, 8, 8>(p, st);
+    return N <= 128 ? run_fwd<T, 16, 8, 8>(p, st) : run_fwd<T, 32, 8, 8>(p, st);
+}
+template <typename T>
+cudaError_t pick_bwd(const BwdArgs &p, cudaStream_t st) {
+    const int64_t N = p.b.fwd.dstate;
+    if (few_rows(p.b.fwd)) return N <= 128 ? run_bwd<T, 4, 8, 32, 4>(p, st) : run_bwd<T, 8, 8, 32, 4>(p, st);
+    if (N <= 32) return run_bwd<T, 4, 8, 8, 8>(p, st);
+    if (N <= 64) return run_bwd<T, 8, 8, 8, 8>(p, st);
+    if (N <= 96) return run_bwd<T, 12, 8, 8, 8>(p, st);
+    return N <= 128 ? run_bwd<T, 16, 8, 8, 8>(p, st) : run_bwd<T, 32, 4, 8, 8>(p, st);
 }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -506,13 +519,7 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 cudaError_t launch_delta_simt(const ssm_delta_args &a, const SeqView &sv, float *ckpt, cudaStream_t st) {
     if (seqs_of(a) == 0) return cudaSuccess;
     const Args p{a, sv, ckpt};
-    const int w = warps_of(a);
-    const bool bf = a.dtype == SSM_BF16;
-    if (a.dstate <= 32) return bf ? pick_fwd<__nv_bfloat16, 4>(p, w, st) : pick_fwd<float, 4>(p, w, st);
-    if (a.dstate <= 64) return bf ? pick_fwd<__nv_bfloat16, 8>(p, w, st) : pick_fwd<float, 8>(p, w, st);
-    if (a.dstate <= 96) return bf ? pick_fwd<__nv_bfloat16, 12>(p, w, st) : pick_fwd<float, 12>(p, w, st);
-    if (a.dstate <= 128) return bf ? pick_fwd<__nv_bfloat16, 16>(p, w, st) : pick_fwd<float, 16>(p, w, st);
-    return bf ? pick_fwd<__nv_bfloat16, 32>(p, w, st) : pick_fwd<float, 32>(p, w, st);
+    return a.dtype == SSM_BF16 ? pick_fwd<__nv_bfloat16>(p, st) : pick_fwd<float>(p, st);
 }
 
 size_t delta_simt_bwd_workspace_bytes(const ssm_delta_bwd_args &b) {
@@ -539,13 +546,8 @@ cudaError_t launch_delta_simt_bwd(const ssm_delta_bwd_args &b, const SeqView &sv
     f.h_final = nullptr;
     cudaError_t e = launch_delta_simt(f, sv, ckpt, st);
     if (e != cudaSuccess) return e;
-    const int w = warps_of(a);
     const bool bf = a.dtype == SSM_BF16;
-    if (a.dstate <= 32) e = bf ? pick_bwd<__nv_bfloat16, 4, 8>(p, w, st) : pick_bwd<float, 4, 8>(p, w, st);
-    else if (a.dstate <= 64) e = bf ? pick_bwd<__nv_bfloat16, 8, 8>(p, w, st) : pick_bwd<float, 8, 8>(p, w, st);
-    else if (a.dstate <= 96) e = bf ? pick_bwd<__nv_bfloat16, 12, 8>(p, w, st) : pick_bwd<float, 12, 8>(p, w, st);
-    else if (a.dstate <= 128) e = bf ? pick_bwd<__nv_bfloat16, 16, 8>(p, w, st) : pick_bwd<float, 16, 8>(p, w, st);
-    else e = bf ? pick_bwd<__nv_bfloat16, 32, 4>(p, w, st) : pick_bwd<float, 32, 4>(p, w, st);
+    e = bf ? pick_bwd<__nv_bfloat16>(p, st) : pick_bwd<float>(p, st);
     if (e != cudaSuccess) return e;
     const int64_t work = a.batch * a.seqlen * a.ngroups * a.dstate;
     if (work == 0) return cudaSuccess;
