@@ -178,37 +178,49 @@ __global__ void __launch_bounds__(W * 32) delta_scan_kernel(const Args p) {
         }
         __syncthreads();
         if (t0 + kTok < sq.hi) fetch(t0 + kTok);
-        for (int t = 0; t < nt; ++t) {
-            // packed pairs of states, two chains a sum
-            const float2 al = make_float2(as[t], as[t]), zero = make_float2(0.f, 0.f);
-            float2 sk2[2] = {zero, zero}, sq2[2] = {zero, zero}, kq2[2] = {zero, zero}, kk[NE / 2];
+        // the next token's operands are on their way while this one's sums run
+        float2 kk[NE / 2], qq[NE / 2];
+        float at, bt, vt;
+        const auto token = [&](int t) {
 #pragma unroll
             for (int e = 0; e < NE / 4; ++e) {
                 const float4 k4 = *reinterpret_cast<const float4 *>(ks + t * NP + state_of<L>(lrow, 4 * e));
+                const float4 q4 = *reinterpret_cast<const float4 *>(qs + t * NP + state_of<L>(lrow, 4 * e));
                 kk[2 * e] = make_float2(k4.x, k4.y);
                 kk[2 * e + 1] = make_float2(k4.z, k4.w);
+                qq[2 * e] = make_float2(q4.x, q4.y);
+                qq[2 * e + 1] = make_float2(q4.z, q4.w);
             }
+            at = as[t];
+            bt = bs[t];
+            vt = vs[t * kRows + r];
+        };
+        token(0);
+        for (int t = 0; t < nt; ++t) {
+            // packed pairs of states, two chains a sum
+            const float2 al = make_float2(at, at), zero = make_float2(0.f, 0.f);
+            float2 sk2[2] = {zero, zero}, sq2[2] = {zero, zero}, kq2[2] = {zero, zero}, k0[NE / 2];
 #pragma unroll
             for (int e = 0; e < NE / 2; ++e) {
+                k0[e] = kk[e];
                 st2[e] = __fmul2_rn(st2[e], al);
                 sk2[e & 1] = __ffma2_rn(st2[e], kk[e], sk2[e & 1]);
+                sq2[e & 1] = __ffma2_rn(st2[e], qq[e], sq2[e & 1]);
+                kq2[e & 1] = __ffma2_rn(kk[e], qq[e], kq2[e & 1]);
             }
-            if (y) {
+            const float b0 = bt, v0 = vt;
+            token(min(t + 1, kTok - 1));
+            const auto part = [](const float2(&x)[2]) { return (x[0].x + x[0].y) + (x[1].x + x[1].y); };
+            float sk = part(sk2), sq_ = part(sq2), kq = part(kq2);
 #pragma unroll
-                for (int e = 0; e < NE / 4; ++e) {
-                    const float4 q4 = *reinterpret_cast<const float4 *>(qs + t * NP + state_of<L>(lrow, 4 * e));
-                    const float2 qa = make_float2(q4.x, q4.y), qb = make_float2(q4.z, q4.w);
-                    sq2[0] = __ffma2_rn(st2[2 * e], qa, sq2[0]);
-                    sq2[1] = __ffma2_rn(st2[2 * e + 1], qb, sq2[1]);
-                    kq2[0] = __ffma2_rn(kk[2 * e], qa, kq2[0]);
-                    kq2[1] = __ffma2_rn(kk[2 * e + 1], qb, kq2[1]);
-                }
+            for (int o = 1; o < L; o <<= 1) {
+                sk += __shfl_xor_sync(~0u, sk, o);
+                sq_ += __shfl_xor_sync(~0u, sq_, o);
+                kq += __shfl_xor_sync(~0u, kq, o);
             }
-            const auto sum = [](const float2(&x)[2]) { return row_sum<L>((x[0].x + x[0].y) + (x[1].x + x[1].y)); };
-            const float sk = sum(sk2), sq_ = y ? sum(sq2) : 0.f, kq = y ? sum(kq2) : 0.f;
-            const float u = bs[t] * (vs[t * kRows + r] - sk);
+            const float u = b0 * (v0 - sk);
 #pragma unroll
-            for (int e = 0; e < NE / 2; ++e) st2[e] = __ffma2_rn(make_float2(u, u), kk[e], st2[e]);
+            for (int e = 0; e < NE / 2; ++e) st2[e] = __ffma2_rn(make_float2(u, u), k0[e], st2[e]);
             if (y && lrow == 0 && live)
                 Elem<T>::st(y + (t0 + t) * a.y_token_stride + r, a.scale * fmaf(u, kq, sq_));
         }
