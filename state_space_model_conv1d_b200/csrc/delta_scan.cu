@@ -334,16 +334,24 @@ __global__ void __launch_bounds__(W * 32, 1) delta_scan_bwd_kernel(const BwdArgs
 #pragma unroll
                 for (int e = 0; e < NE; ++e) st[e] = 0.f;
             // forward to the run's first token
-            for (int t = 0; t < run * TR; ++t) {
-                float sk = 0.f;
+            {
+                float kn[NE];
 #pragma unroll
-                for (int e = 0; e < NE; ++e) {
-                    st[e] *= as[t];
-                    sk = fmaf(st[e], ks[t * NP + state_of<L>(lrow, e)], sk);
+                for (int e = 0; e < NE; ++e) kn[e] = ks[state_of<L>(lrow, e)];
+                for (int t = 0; t < run * TR; ++t) {
+                    float sk = 0.f, kt[NE];
+                    const float at = as[t];
+#pragma unroll
+                    for (int e = 0; e < NE; ++e) {
+                        kt[e] = kn[e];
+                        st[e] *= at;
+                        sk = fmaf(st[e], kt[e], sk);
+                        kn[e] = ks[(t + 1) * NP + state_of<L>(lrow, e)];       // t + 1 < kTok
+                    }
+                    const float u = bs[t] * (vs[t * kRows + r] - row_sum<L>(sk));
+#pragma unroll
+                    for (int e = 0; e < NE; ++e) st[e] = fmaf(u, kt[e], st[e]);
                 }
-                const float u = bs[t] * (vs[t * kRows + r] - row_sum<L>(sk));
-#pragma unroll
-                for (int e = 0; e < NE; ++e) st[e] = fmaf(u, ks[t * NP + state_of<L>(lrow, e)], st[e]);
             }
             // through the run: w = a h_{t-1} of every token stays in registers
             float w[TR][NE], uu[TR], sk_[TR];
@@ -518,7 +526,7 @@ cudaError_t pick_fwd(const Args &p, cudaStream_t st) {
 template <typename T>
 cudaError_t pick_bwd(const BwdArgs &p, cudaStream_t st) {
     const int64_t N = p.b.fwd.dstate;
-    if (few_rows(p.b.fwd)) return N <= 128 ? run_bwd<T, 4, 8, 32, 4>(p, st) : run_bwd<T, 8, 8, 32, 4>(p, st);
+    if (few_rows(p.b.fwd)) return N <= 128 ? run_bwd<T, 4, 16, 32, 4>(p, st) : run_bwd<T, 8, 8, 32, 4>(p, st);
     if (N <= 32) return run_bwd<T, 4, 8, 8, 8>(p, st);
     if (N <= 64) return run_bwd<T, 8, 8, 8, 8>(p, st);
     if (N <= 96) return run_bwd<T, 12, 8, 8, 8>(p, st);
