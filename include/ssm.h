@@ -430,7 +430,9 @@ SSM_API ssm_status ssm_split_fixup(const ssm_scan_args *args, const float *cum_d
  * beta in [0, 1]; other values are computed as the formula stands.  g <= 0 is
  * the log decay; g below -100 (-infinity included) counts as -100, whose
  * exp() is zero in fp32.  A NaN or infinity reaches the other tokens of its
- * own 64-token block and everything after it, never another sequence.
+ * own 64-token block and everything after it (before it, in the gradients),
+ * never another sequence.  Outputs may not overlap inputs or each other,
+ * except that h_final may be h0.
  *
  * q, k, v, y share one dtype; g and beta are fp32 whatever the dtype, since a
  * log decay summed over a sequence does not survive 8 bits.  bf16 with
@@ -490,8 +492,11 @@ typedef struct ssm_delta_update_args {
     int64_t nslots;
 } ssm_delta_update_args;
 
-/* `workspace`: device, 256-byte aligned, ssm_delta_workspace_size() bytes;
- * its error word is read with ssm_workspace_error. */
+/* `workspace`: device, 256-byte aligned, ssm_delta_workspace_size() bytes
+ * (shapes alone decide them); its error word is read with
+ * ssm_workspace_error.  ssm_delta_bwd_workspace_size wants the pointers and
+ * strides of the call too: their alignment decides the path and with it the
+ * size.  Calls that may run at the same time need workspaces of their own. */
 SSM_API size_t ssm_delta_workspace_size(const ssm_delta_args *args);
 SSM_API ssm_status ssm_delta_fwd(const ssm_delta_args *args, void *workspace, size_t ws_bytes, void *stream);
 SSM_API size_t ssm_delta_bwd_workspace_size(const ssm_delta_bwd_args *args);
@@ -511,7 +516,8 @@ SSM_API ssm_status ssm_delta_update(const ssm_delta_update_args *args, void *str
  *     y   = t | silu(t) | t * silu(z)            SSM_NORM_PLAIN, _GATE_FIRST | _SILU | _GATE
  *
  * Statistics and arithmetic are fp32; y is rounded once.  channels / groups
- * is at most 16384.  y may be x (same strides). */
+ * is at most 16384.  y may be x (same strides); other outputs may not overlap
+ * inputs. */
 typedef enum { SSM_NORM_PLAIN = 0, SSM_NORM_SILU = 1, SSM_NORM_GATE = 2, SSM_NORM_GATE_FIRST = 3 } ssm_norm_mode;
 typedef struct ssm_norm_args {
     int32_t dtype;            /* ssm_dtype of x, z, y */
@@ -553,6 +559,7 @@ SSM_API ssm_status ssm_group_norm_bwd(const ssm_norm_bwd_args *args, void *works
  *   fork     for every entry in order: pages[i] = the lowest free page, refs
  *            = 1, its contents those of page src[i] (which has to be live) or
  *            zeros for src[i] = -1.  pages[i] = -1 when no page is left.
+ *            pages may be src.
  *   free     refs[pages[i]] -= 1 for pages[i] >= 0.  Contents stay.
  *   compact  with n live pages, the i-th live page at or behind n moves to
  *            the i-th free page before n; refs follow, and table[j] (page

@@ -8,6 +8,7 @@ namespace ssm {
 // exp() of a log decay at or below this is zero in fp32; clamping there keeps
 // a full reset (g = -infinity) out of the prefix sums, where it would give NaN.
 constexpr float kMinLogDecay = -100.f;
+__device__ __forceinline__ float log_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }   // (a NaN stays one)
 
 // Token-by-token path (any dtype and sizes).  `ckpt` (may be null) receives
 // the state before every kDeltaCkpt-th token of each sequence.

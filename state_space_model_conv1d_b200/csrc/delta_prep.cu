@@ -267,8 +267,8 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
             Gates &gt = sm.gates[w - 2];
             const int h = h0 + hb + w - 2;
             const float *gp = p.g + b.row * p.g_bs + b.t0 * p.g_ts + h, *bp = p.beta + b.row * p.b_bs + b.t0 * p.b_ts + h;
-            const float g0 = lane < b.nt ? fmaxf(gp[lane * p.g_ts], kMinLogDecay) : 0.f;
-            const float g1 = lane + 32 < b.nt ? fmaxf(gp[(lane + 32) * p.g_ts], kMinLogDecay) : 0.f;
+            const float g0 = lane < b.nt ? log_decay(gp[lane * p.g_ts]) : 0.f;
+            const float g1 = lane + 32 < b.nt ? log_decay(gp[(lane + 32) * p.g_ts]) : 0.f;
             float b0 = lane < b.nt ? bp[lane * p.b_ts] : 0.f, b1 = lane + 32 < b.nt ? bp[(lane + 32) * p.b_ts] : 0.f;
             if (p.bwd) {
                 b0 = bwd_beta(b0);

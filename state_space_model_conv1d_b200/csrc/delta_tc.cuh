@@ -39,7 +39,7 @@ struct Rec {
 // beta of the backward: dbeta_i = dR_i . u_i / beta_i, and u_i / beta_i stays
 // exact for a beta so small that nothing else notices it.
 constexpr float kTinyBeta = 1e-20f;
-SSM_DEVINL float bwd_beta(float b) { return b == 0.f ? kTinyBeta : b; }
+SSM_DEVINL float bwd_beta(float b) { return fabsf(b) < kTinyBeta ? copysignf(kTinyBeta, b) : b; }
 
 // The first 1024-byte boundary of the dynamic shared memory, by an offset: a
 // pointer made from an integer would turn every access into a generic one.

@@ -571,7 +571,7 @@ delta_bwd_chain_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, c
                     bv[1][0] = bv[0][0]; bv[1][1] = bv[0][1];
                 }
                 double cs[2], last;
-                block_cs(fmaxf(gv[hh][0], kMinLogDecay), fmaxf(gv[hh][1], kMinLogDecay), cs[0], cs[1], last);
+                block_cs(log_decay(gv[hh][0]), log_decay(gv[hh][1]), cs[0], cs[1], last);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int t = lane + 32 * e;
@@ -726,8 +726,8 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
             const float *gp = a.g + blk.row * a.g_batch_stride + blk.t0 * a.g_token_stride + head;
             const float *bp = a.beta + blk.row * a.beta_batch_stride + blk.t0 * a.beta_token_stride + head;
             double cs[2], last;
-            block_cs(lane < nt ? fmaxf(gp[lane * a.g_token_stride], kMinLogDecay) : 0.f,
-                     lane + 32 < nt ? fmaxf(gp[(lane + 32) * a.g_token_stride], kMinLogDecay) : 0.f, cs[0], cs[1], last);
+            block_cs(lane < nt ? log_decay(gp[lane * a.g_token_stride]) : 0.f,
+                     lane + 32 < nt ? log_decay(gp[(lane + 32) * a.g_token_stride]) : 0.f, cs[0], cs[1], last);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int t = lane + 32 * e;

@@ -541,7 +541,7 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
                     bv[1][0] = bv[0][0]; bv[1][1] = bv[0][1];
                 }
                 double cs[2], last;
-                block_cs(fmaxf(gv[hh][0], kMinLogDecay), fmaxf(gv[hh][1], kMinLogDecay), cs[0], cs[1], last);
+                block_cs(log_decay(gv[hh][0]), log_decay(gv[hh][1]), cs[0], cs[1], last);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int t = lane + 32 * e;
@@ -585,7 +585,8 @@ cudaError_t run(const Args &p, dim3 grid, const DeltaMaps &m, cudaStream_t st) {
 }  // namespace
 
 bool delta_tc_shape(const ssm_delta_args &a) {
-    return a.dtype == SSM_BF16 && a.dstate <= 128 && a.dstate % 8 == 0 && a.headdim % 8 == 0 && a.nheads <= 65535;
+    return a.dtype == SSM_BF16 && a.dstate <= 128 && a.dstate % 8 == 0 && a.headdim % 8 == 0 && a.nheads <= 65535 &&
+           a.nheads * a.headdim <= INT32_MAX;
 }
 namespace {
 bool al16(const void *p, int64_t bs = 0, int64_t ts = 0) { return ((uintptr_t)p % 16) == 0 && bs % 8 == 0 && ts % 8 == 0; }

@@ -109,15 +109,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PageOp op, const ssm
                                  [&](int64_t p, int rank) { w.mark[rank] = (int)p; });
         __syncthreads();
         const auto valid = [&](int64_t i) {
-            const int s = a.src[i];
+            const int s = w.from[i];
             return s == -1 || (s >= 0 && s < ns && a.refs[s] > 0);
         };
         for (int64_t i = tid; i < a.n; i += kPlanThreads) {
-            const bool ok = valid(i);
-            if (!ok) bad = 1;
+            w.from[i] = a.src[i];                      // (pages may be src)
             a.pages[i] = -1;
-            w.from[i] = a.src[i];
             w.to[i] = -1;
+            if (!valid(i)) bad = 1;
         }
         __syncthreads();
         ranked(a.n, sm, valid, [&](int64_t i, int rank) {

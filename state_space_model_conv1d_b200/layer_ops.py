@@ -109,10 +109,13 @@ def _workspace(workspace, need, like, idx):
 
 
 # ------------------------------------------------------------ gated delta rule
-def _delta_args(q, k, v, g, beta, y, y_name, scale, h0, h_final, cu_seqlens):
-    """The fields of ``ssm_delta_args`` in order, and the number of sequences."""
+def _check_dims(q, v):
     if v.dim() != 4 or q.dim() != 4:
         raise ValueError("q, k are [b, T, G, N] and v is [b, T, H, P]")
+
+
+def _delta_args(q, k, v, g, beta, y, y_name, scale, h0, h_final, cu_seqlens):
+    """The fields of ``ssm_delta_args`` in order, and the number of sequences."""
     idx, dt = v.get_device(), v.dtype
     b, T, H, P = v.shape
     G, N = q.shape[2], q.shape[3]
@@ -145,6 +148,7 @@ def delta_fwd(q, k, v, g, beta, *, scale=None, h0=None, cu_seqlens=None, y=None,
 
 
 def _delta_fwd(q, k, v, g, beta, scale, h0, cu_seqlens, y, h_final, return_final_state, workspace, s):
+    _check_dims(q, v)
     if y is None:
         y = _new(v)
     if h_final is None and return_final_state:
@@ -169,6 +173,7 @@ def delta_bwd(q, k, v, g, beta, dy, *, scale=None, h0=None, cu_seqlens=None, dh_
 
 
 def _delta_bwd(q, k, v, g, beta, dy, scale, h0, cu_seqlens, dh_final, out, workspace, s):
+    _check_dims(q, v)
     fwd, nseq = _delta_args(q, k, v, g, beta, dy, "dy", scale, h0, None, cu_seqlens)
     idx, dt = v.get_device(), v.dtype
     hshape = (nseq, v.shape[2], v.shape[3], q.shape[3])
