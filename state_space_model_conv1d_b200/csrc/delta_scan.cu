@@ -449,6 +449,222 @@ __global__ void __launch_bounds__(W * 32, 1) delta_scan_bwd_kernel(const BwdArgs
     }
 }
 
+// Sum over the rows of a warp of 4 values per lane (one row, or two rows of 16
+// lanes, which end with two values each), and where they go.
+template <int L> constexpr int kRowKept = L == 32 ? 4 : 2;
+template <int L> SSM_DEVINL void pair_sum(const float (&x)[4], float (&out)[kRowKept<L>], int lane) {
+    static_assert(L == 32 || L == 16, "one or two rows a warp");
+    if constexpr (L == 32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] = x[e];
+    } else {
+        const bool hi = lane & 16;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) out[e] = (hi ? x[e + 2] : x[e]) + __shfl_xor_sync(~0u, hi ? x[e] : x[e + 2], 16);
+    }
+}
+template <int L> SSM_DEVINL void keep_pair(float *dst, const float (&v)[kRowKept<L>], int lane) {
+    if constexpr (L == 32) *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+    else *reinterpret_cast<float2 *>(dst + (lane & 16 ? 2 : 0)) = make_float2(v[0], v[1]);
+}
+
+// The same for few rows and dstate <= 4 L: w = a h_{t-1} of all 32 tokens between
+// two checkpoints fits in shared memory, so the states are walked once, in loops
+// short enough for the instruction cache.  The next token's operands are read
+// while a token's sum runs, the next tokens' rows while the tokens before are in
+// work.  The shares of kGroup tokens at a time are added over the CTA's warps,
+// out of two buffers in turn.
+constexpr int kGroup = 8;
+template <int L, int W> constexpr int rows_bwd_floats() {
+    constexpr int NP = 4 * L, R = Cut<L, W>::rows, K = kDeltaCkpt;
+    return 2 * K * NP + K * R * NP + 4 * K * R + 2 * K + 2 * kGroup * (2 * W * NP + W * 32 + R);
+}
+
+template <typename T, int L, int W>
+__global__ void __launch_bounds__(W * 32, 1) delta_rows_bwd_kernel(const BwdArgs p) {
+    constexpr int kThreads = W * 32, kRows = Cut<L, W>::rows, kTok = kDeltaCkpt, NE = 4, NP = NE * L;
+    const ssm_delta_args &a = p.b.fwd;
+    if (p.sv.err && *p.sv.err != 0) return;
+    extern __shared__ float sm[];
+    float *ks = sm, *qs = ks + kTok * NP, *ws = qs + kTok * NP;        // ws [kTok][kRows][NP]
+    float *vs = ws + kTok * kRows * NP, *ds = vs + kTok * kRows, *us = ds + kTok * kRows, *es = us + kTok * kRows;
+    float *as = es + kTok * kRows, *bs = as + kTok;
+    float *rq = bs + kTok, *rk = rq + 2 * kGroup * W * NP;             // [2][kGroup][W][NP]
+    float *rg = rk + 2 * kGroup * W * NP, *rb = rg + 2 * kGroup * kThreads;    // [2][kGroup][threads], [2][kGroup][kRows]
+    const Seq sq = find_seq(a, p.sv, blockIdx.y);
+    const int64_t H = a.nheads, P = a.headdim, N = a.dstate;
+    const int h = blockIdx.x % H, slice = (int)(blockIdx.x / H), p0 = slice * kRows;
+    const int grp = (int)(h / (H / a.ngroups));
+    if (!SSM_BOUNDS(sq.hi, a.seqlen + 1, BS_DELTA_SEQ) || !SSM_BOUNDS(sq.lo, sq.hi + 1, BS_DELTA_SEQ)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lrow = lane % L;
+    const int r = warp * Cut<L, W>::per_warp + lane / L, n0 = lrow * 4;    // this lane's row and first state
+    const bool live = p0 + r < P;
+    const int64_t srow = ((int64_t)sq.s * H + h) * P + p0 + r;
+    float d[NE] = {0.f, 0.f, 0.f, 0.f};
+    if (live && p.b.dh_final) load_row<NE, L>(d, p.b.dh_final + srow * N, lrow, N);
+    const T *q = (const T *)a.q + sq.row * a.q_batch_stride + grp * N;
+    const T *k = (const T *)a.k + sq.row * a.k_batch_stride + grp * N;
+    const T *v = (const T *)a.v + sq.row * a.v_batch_stride + h * P + p0;
+    const T *dy = (const T *)p.b.dy + sq.row * p.b.dy_batch_stride + h * P + p0;
+    const float *g = a.g + sq.row * a.g_batch_stride + h, *be = a.beta + sq.row * a.beta_batch_stride + h;
+    const int64_t tok0 = sq.row * a.seqlen, ntok = a.batch * a.seqlen;
+    T *dv = (T *)p.b.dv + h * P + p0;
+    const int vw = (int)min((int64_t)kRows, P - p0);
+    const int64_t len = sq.hi - sq.lo, chunks = (len + kTok - 1) / kTok;
+
+    Staged<T, NP, kTok, kThreads> sk, sq_;
+    Staged<T, kRows, kTok, kThreads> sv, sd;
+    float ga = 1.f, gb = 0.f, st0[NE];
+    const auto fetch = [&](int64_t c) {
+        const int64_t t0 = sq.lo + c * kTok;
+        const int nt = (int)min((int64_t)kTok, sq.hi - t0);
+        sk.load(k + t0 * a.k_token_stride, a.k_token_stride, nt, (int)N);
+        sq_.load(q + t0 * a.q_token_stride, a.q_token_stride, nt, (int)N);
+        sv.load(v + t0 * a.v_token_stride, a.v_token_stride, nt, vw);
+        sd.load(dy + t0 * p.b.dy_token_stride, p.b.dy_token_stride, nt, vw);
+        if (threadIdx.x < kTok) {
+            const int t = threadIdx.x;
+            ga = t < nt ? g[(t0 + t) * a.g_token_stride] : 0.f;
+            gb = t < nt ? be[(t0 + t) * a.beta_token_stride] : 0.f;
+        }
+        if (live) load_row<NE, L>(st0, p.ckpt + (((sq.ckpt_row + c) * H + h) * P + p0 + r) * N, lrow, N);
+        else
+#pragma unroll
+            for (int e = 0; e < NE; ++e) st0[e] = 0.f;
+    };
+    const auto at4 = [&](const float *x) { return *reinterpret_cast<const float4 *>(x + n0); };
+    if (chunks > 0) fetch(chunks - 1);
+    for (int64_t c = chunks - 1; c >= 0; --c) {
+        const int64_t t0 = sq.lo + c * kTok;
+        const int nt = (int)min((int64_t)kTok, sq.hi - t0);
+        __syncthreads();                               // the tokens before are done with
+        sk.store(ks);
+        sq_.store(qs);
+        sv.store(vs);
+        sd.store(ds);
+        if (threadIdx.x < kTok) {
+            as[threadIdx.x] = decay_of(ga);
+            bs[threadIdx.x] = gb;
+        }
+        float st[NE];
+#pragma unroll
+        for (int e = 0; e < NE; ++e) st[e] = st0[e];
+        __syncthreads();
+        if (c > 0) fetch(c - 1);
+        {   // w, u and v - w k of every token
+            float4 kn = at4(ks);
+            float an = as[0], bn = bs[0], vn = vs[r];
+#pragma unroll 2
+            for (int t = 0; t < nt; ++t) {
+                const float4 k4 = kn;
+                const float bt = bn, vt = vn;
+                const float4 w = make_float4(st[0] * an, st[1] * an, st[2] * an, st[3] * an);
+                const int tn = min(t + 1, kTok - 1);
+                kn = at4(ks + tn * NP);
+                an = as[tn];
+                bn = bs[tn];
+                vn = vs[tn * kRows + r];
+                *reinterpret_cast<float4 *>(ws + (t * kRows + r) * NP + n0) = w;
+                const float e = vt - row_sum<L>(fmaf(w.x, k4.x, w.y * k4.y) + fmaf(w.z, k4.z, w.w * k4.w));
+                const float u = bt * e;
+                st[0] = fmaf(u, k4.x, w.x);
+                st[1] = fmaf(u, k4.y, w.y);
+                st[2] = fmaf(u, k4.z, w.z);
+                st[3] = fmaf(u, k4.w, w.w);
+                if (lrow == 0) {
+                    us[t * kRows + r] = u;
+                    es[t * kRows + r] = e;
+                }
+            }
+        }
+        __syncwarp();                                  // (rows, and with them us and es, belong to one warp)
+        float4 kn, qn, wn;
+        float an, bn, un, en, yn;
+        const auto token = [&](int t) {
+            kn = at4(ks + t * NP);
+            qn = at4(qs + t * NP);
+            wn = at4(ws + (t * kRows + r) * NP);
+            an = as[t];
+            bn = bs[t];
+            un = us[t * kRows + r];
+            en = es[t * kRows + r];
+            yn = a.scale * ds[t * kRows + r];
+        };
+        token(nt - 1);
+        for (int grp8 = (nt - 1) / kGroup; grp8 >= 0; --grp8) {
+            const int buf = grp8 & 1, first = grp8 * kGroup, cnt = min(kGroup, nt - first);
+            float *bq = rq + buf * kGroup * W * NP, *bk = rk + buf * kGroup * W * NP, *bg = rg + buf * kGroup * kThreads,
+                  *bb = rb + buf * kGroup * kRows;
+#pragma unroll 2
+            for (int i = cnt - 1; i >= 0; --i) {
+                const int t = first + i;
+                const float kk[NE] = {kn.x, kn.y, kn.z, kn.w}, qq[NE] = {qn.x, qn.y, qn.z, qn.w},
+                            w[NE] = {wn.x, wn.y, wn.z, wn.w};
+                const float al = an, bt = bn, u = un, ev = en, dyv = yn;
+                token(max(t - 1, 0));
+                float x[NE], part[kRowKept<L>];
+#pragma unroll
+                for (int e = 0; e < NE; ++e) d[e] = fmaf(dyv, qq[e], d[e]);
+                const float du = row_sum<L>(fmaf(d[0], kk[0], d[1] * kk[1]) + fmaf(d[2], kk[2], d[3] * kk[3]));
+                const int slot = (i * W + warp) * NP + n0;
+#pragma unroll
+                for (int e = 0; e < NE; ++e) x[e] = dyv * fmaf(u, kk[e], w[e]);        // dq: dy h_t
+                pair_sum<L>(x, part, lane);
+                keep_pair<L>(bq + slot, part, lane);
+                const float dsv = -bt * du;
+                float dg = 0.f;
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    x[e] = fmaf(u, d[e], dsv * w[e]);
+                    d[e] = fmaf(dsv, kk[e], d[e]);
+                    dg = fmaf(d[e], w[e], dg);
+                    d[e] *= al;
+                }
+                pair_sum<L>(x, part, lane);
+                keep_pair<L>(bk + slot, part, lane);
+                bg[i * kThreads + threadIdx.x] = dg;
+                if (lrow == 0) {
+                    bb[i * kRows + r] = du * ev;
+                    if (live) Elem<T>::st(dv + (tok0 + t0 + t) * H * P + r, -dsv);
+                }
+            }
+            __syncthreads();                           // (the other buffer's readers are past the one before)
+            for (int i = threadIdx.x; i < cnt * NP; i += kThreads) {
+                const int ti = i / NP, n = i % NP;
+                if (n >= N) continue;
+                float sqv = 0.f, skv = 0.f;
+#pragma unroll
+                for (int wv = 0; wv < W; ++wv) {
+                    sqv += bq[(ti * W + wv) * NP + n];
+                    skv += bk[(ti * W + wv) * NP + n];
+                }
+                const int64_t at = (((int64_t)slice * ntok + tok0 + t0 + first + ti) * H + h) * N + n;
+                p.pq[at] = sqv;
+                p.pk[at] = skv;
+            }
+            for (int ti = warp; ti < cnt; ti += W) {
+                float sg = 0.f, sb = lane < kRows ? bb[ti * kRows + lane] : 0.f;
+#pragma unroll
+                for (int i = 0; i < W; ++i) sg += bg[ti * kThreads + i * 32 + lane];
+#pragma unroll
+                for (int o = 16; o; o >>= 1) {
+                    sg += __shfl_xor_sync(~0u, sg, o);
+                    sb += __shfl_xor_sync(~0u, sb, o);
+                }
+                if (lane == 0) {
+                    const int64_t at = ((int64_t)slice * ntok + tok0 + t0 + first + ti) * H + h;
+                    p.pg[at] = sg;
+                    p.pb[at] = sb;
+                }
+            }
+        }
+    }
+    if (live && p.b.dh0)
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+            if (n0 + e < N) p.b.dh0[srow * N + n0 + e] = d[e];
+}
+
 // Adds the shares of the row slices and, for dq / dk, of a group's heads.
 template <typename T>
 __global__ void delta_shares_kernel(const BwdArgs p, int slices) {
@@ -507,16 +723,30 @@ cudaError_t run_bwd(const BwdArgs &p, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+template <typename T, int L, int W>
+cudaError_t run_rows_bwd(const BwdArgs &p, cudaStream_t st) {
+    constexpr int kRows = Cut<L, W>::rows;
+    const ssm_delta_args &a = p.b.fwd;
+    const dim3 grid((unsigned)(a.nheads * ((a.headdim + kRows - 1) / kRows)), (unsigned)(a.cu_seqlens ? a.nseqs : a.batch));
+    constexpr size_t smem = (size_t)rows_bwd_floats<L, W>() * 4;
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    cudaError_t e = set_smem(delta_rows_bwd_kernel<T, L, W>, smem);
+    if (e != cudaSuccess) return e;
+    delta_rows_bwd_kernel<T, L, W><<<grid, W * 32, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
 int64_t seqs_of(const ssm_delta_args &a) { return a.cu_seqlens ? a.nseqs : a.batch; }
 // Few rows: with 4 of them a warp, less than a warp for each of the GPU's schedulers.
 bool few_rows(const ssm_delta_args &a) { return seqs_of(a) * a.nheads * a.headdim < 4LL * 4 * sm_count(); }
 int64_t slices_of(const ssm_delta_args &a) {
-    const int rows = few_rows(a) ? Cut<32, 4>::rows : Cut<8, 8>::rows;
+    const int rows = !few_rows(a) ? Cut<8, 8>::rows : a.dstate <= 64 ? Cut<16, 4>::rows : Cut<32, 4>::rows;
     return (a.headdim + rows - 1) / rows;
 }
 template <typename T>
 cudaError_t pick_fwd(const Args &p, cudaStream_t st) {
     const int64_t N = p.a.dstate;
+    if (few_rows(p.a) && N <= 64) return run_fwd<T, 4, 16, 4>(p, st);
     if (few_rows(p.a)) return N <= 128 ? run_fwd<T, 4, 32, 4>(p, st) : run_fwd<T, 8, 32, 4>(p, st);
     if (N <= 32) return run_fwd<T, 4, 8, 8>(p, st);
     if (N <= 64) return run_fwd<T, 8, 8, 8>(p, st);
@@ -526,7 +756,8 @@ cudaError_t pick_fwd(const Args &p, cudaStream_t st) {
 template <typename T>
 cudaError_t pick_bwd(const BwdArgs &p, cudaStream_t st) {
     const int64_t N = p.b.fwd.dstate;
-    if (few_rows(p.b.fwd)) return N <= 128 ? run_bwd<T, 4, 16, 32, 4>(p, st) : run_bwd<T, 8, 8, 32, 4>(p, st);
+    if (few_rows(p.b.fwd) && N <= 64) return run_rows_bwd<T, 16, 4>(p, st);
+    if (few_rows(p.b.fwd)) return N <= 128 ? run_rows_bwd<T, 32, 4>(p, st) : run_bwd<T, 8, 8, 32, 4>(p, st);
     if (N <= 32) return run_bwd<T, 4, 8, 8, 8>(p, st);
     if (N <= 64) return run_bwd<T, 8, 8, 8, 8>(p, st);
     if (N <= 96) return run_bwd<T, 12, 8, 8, 8>(p, st);
