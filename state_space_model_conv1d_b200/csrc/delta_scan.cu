@@ -110,14 +110,20 @@ template <int L> SSM_DEVINL float row_sum(float v) {
     return v;
 }
 
-template <typename T, int NE, int L, int W>
+// Y: y is wanted (the checkpoints alone otherwise).  Only the sum that the chain
+// waits for is taken at once; y's partial sums, one per lane and token, go to a
+// tile of the warp's own and are added after kTok tokens, a token in each lane.
+template <int NE, int L, int W, bool Y> constexpr int scan_floats() {
+    return (Y ? 2 : 1) * kDeltaCkpt * NE * L + kDeltaCkpt * (Cut<L, W>::rows + 2) + (Y ? W * 32 * 33 : 0);
+}
+template <typename T, int NE, int L, int W, bool Y>
 __global__ void __launch_bounds__(W * 32) delta_scan_kernel(const Args p) {
     constexpr int kThreads = Cut<L, W>::threads, kRows = Cut<L, W>::rows, kTok = kDeltaCkpt;   // tokens staged at a time
     const ssm_delta_args &a = p.a;
     if (p.sv.err && *p.sv.err != 0) return;
     constexpr int NP = NE * L;
     extern __shared__ float sm[];
-    float *ks = sm, *qs = ks + kTok * NP, *vs = qs + kTok * NP, *as = vs + kTok * kRows, *bs = as + kTok;
+    float *ks = sm, *qs = ks + kTok * NP, *vs = Y ? qs + kTok * NP : qs, *as = vs + kTok * kRows, *bs = as + kTok;
     const Seq sq = find_seq(a, p.sv, blockIdx.y);
     const int64_t H = a.nheads, P = a.headdim, N = a.dstate;
     const int h = blockIdx.x % H, p0 = (int)(blockIdx.x / H) * kRows;
@@ -147,7 +153,8 @@ __global__ void __launch_bounds__(W * 32) delta_scan_kernel(const Args p) {
     const T *k = (const T *)a.k + sq.row * a.k_batch_stride + grp * N;
     const T *v = (const T *)a.v + sq.row * a.v_batch_stride + h * P + p0;
     const float *g = a.g + sq.row * a.g_batch_stride + h, *be = a.beta + sq.row * a.beta_batch_stride + h;
-    T *y = a.y ? (T *)a.y + sq.row * a.y_batch_stride + h * P + p0 : nullptr;
+    T *y = Y ? (T *)a.y + sq.row * a.y_batch_stride + h * P + p0 + warp * Cut<L, W>::per_warp : nullptr;
+    float *ys = bs + kTok + warp * 32 * 33;            // [token][lane]
     const int vw = (int)min((int64_t)kRows, P - p0);
     Staged<T, NP, kTok, kThreads> sk_, sq_s;
     Staged<T, kRows, kTok, kThreads> sv_;
@@ -155,7 +162,7 @@ __global__ void __launch_bounds__(W * 32) delta_scan_kernel(const Args p) {
     const auto fetch = [&](int64_t t0) {
         const int nt = (int)min((int64_t)kTok, sq.hi - t0);
         sk_.load(k + t0 * a.k_token_stride, a.k_token_stride, nt, (int)N);
-        if (y) sq_s.load(q + t0 * a.q_token_stride, a.q_token_stride, nt, (int)N);
+        if constexpr (Y) sq_s.load(q + t0 * a.q_token_stride, a.q_token_stride, nt, (int)N);
         sv_.load(v + t0 * a.v_token_stride, a.v_token_stride, nt, vw);
         if (threadIdx.x < kTok) {
             const int t = threadIdx.x;
@@ -170,7 +177,7 @@ __global__ void __launch_bounds__(W * 32) delta_scan_kernel(const Args p) {
             keep(p.ckpt + (((sq.ckpt_row + (t0 - sq.lo) / kDeltaCkpt) * H + h) * P + p0 + r) * N);
         __syncthreads();                               // the tokens before are read
         sk_.store(ks);
-        if (y) sq_s.store(qs);
+        if constexpr (Y) sq_s.store(qs);
         sv_.store(vs);
         if (threadIdx.x < kTok) {
             as[threadIdx.x] = decay_of(ga);
@@ -178,51 +185,63 @@ __global__ void __launch_bounds__(W * 32) delta_scan_kernel(const Args p) {
         }
         __syncthreads();
         if (t0 + kTok < sq.hi) fetch(t0 + kTok);
-        // the next token's operands are on their way while this one's sums run
+        // the next token's operands are on their way while this one's sum runs
         float2 kk[NE / 2], qq[NE / 2];
         float at, bt, vt;
-        const auto token = [&](int t) {
+        const auto pairs = [&](float2(&x)[NE / 2], const float *row) {
 #pragma unroll
             for (int e = 0; e < NE / 4; ++e) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(ks + t * NP + state_of<L>(lrow, 4 * e));
-                const float4 q4 = *reinterpret_cast<const float4 *>(qs + t * NP + state_of<L>(lrow, 4 * e));
-                kk[2 * e] = make_float2(k4.x, k4.y);
-                kk[2 * e + 1] = make_float2(k4.z, k4.w);
-                qq[2 * e] = make_float2(q4.x, q4.y);
-                qq[2 * e + 1] = make_float2(q4.z, q4.w);
+                const float4 u = *reinterpret_cast<const float4 *>(row + state_of<L>(lrow, 4 * e));
+                x[2 * e] = make_float2(u.x, u.y);
+                x[2 * e + 1] = make_float2(u.z, u.w);
             }
+        };
+        const auto token = [&](int t) {
+            pairs(kk, ks + t * NP);
             at = as[t];
             bt = bs[t];
             vt = vs[t * kRows + r];
         };
+        const auto part = [](const float2(&x)[2]) { return (x[0].x + x[0].y) + (x[1].x + x[1].y); };
         token(0);
         for (int t = 0; t < nt; ++t) {
             // packed pairs of states, two chains a sum
             const float2 al = make_float2(at, at), zero = make_float2(0.f, 0.f);
-            float2 sk2[2] = {zero, zero}, sq2[2] = {zero, zero}, kq2[2] = {zero, zero}, k0[NE / 2];
+            float2 sk2[2] = {zero, zero}, k0[NE / 2];
 #pragma unroll
             for (int e = 0; e < NE / 2; ++e) {
                 k0[e] = kk[e];
                 st2[e] = __fmul2_rn(st2[e], al);
                 sk2[e & 1] = __ffma2_rn(st2[e], kk[e], sk2[e & 1]);
-                sq2[e & 1] = __ffma2_rn(st2[e], qq[e], sq2[e & 1]);
-                kq2[e & 1] = __ffma2_rn(kk[e], qq[e], kq2[e & 1]);
             }
             const float b0 = bt, v0 = vt;
+            if constexpr (Y) pairs(qq, qs + t * NP);
             token(min(t + 1, kTok - 1));
-            const auto part = [](const float2(&x)[2]) { return (x[0].x + x[0].y) + (x[1].x + x[1].y); };
-            float sk = part(sk2), sq_ = part(sq2), kq = part(kq2);
-#pragma unroll
-            for (int o = 1; o < L; o <<= 1) {
-                sk += __shfl_xor_sync(~0u, sk, o);
-                sq_ += __shfl_xor_sync(~0u, sq_, o);
-                kq += __shfl_xor_sync(~0u, kq, o);
-            }
-            const float u = b0 * (v0 - sk);
+            const float u = b0 * (v0 - row_sum<L>(part(sk2)));
 #pragma unroll
             for (int e = 0; e < NE / 2; ++e) st2[e] = __ffma2_rn(make_float2(u, u), k0[e], st2[e]);
-            if (y && lrow == 0 && live)
-                Elem<T>::st(y + (t0 + t) * a.y_token_stride + r, a.scale * fmaf(u, kq, sq_));
+            if constexpr (Y) {
+                float2 sy[2] = {zero, zero};
+#pragma unroll
+                for (int e = 0; e < NE / 2; ++e) sy[e & 1] = __ffma2_rn(st2[e], qq[e], sy[e & 1]);
+                ys[t * 33 + lane] = part(sy);
+            }
+        }
+        if constexpr (Y) {
+            __syncwarp();
+            if (lane < nt)
+#pragma unroll
+                for (int i = 0; i < Cut<L, W>::per_warp; ++i) {
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int e = 0; e < L; e += 2) {
+                        s0 += ys[lane * 33 + i * L + e];
+                        s1 += ys[lane * 33 + i * L + e + 1];
+                    }
+                    if (p0 + warp * Cut<L, W>::per_warp + i < P)
+                        Elem<T>::st(y + (t0 + lane) * a.y_token_stride + i, a.scale * (s0 + s1));
+                }
+            __syncwarp();
         }
     }
     if (a.h_final && live) keep(a.h_final + srow * N);
@@ -700,16 +719,20 @@ cudaError_t set_smem(K kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, int NE, int L, int W>
-cudaError_t run_fwd(const Args &p, cudaStream_t st) {
-    constexpr int kTok = kDeltaCkpt, kRows = Cut<L, W>::rows;
+template <typename T, int NE, int L, int W, bool Y>
+cudaError_t run_scan(const Args &p, cudaStream_t st) {
+    constexpr int kRows = Cut<L, W>::rows;
     const ssm_delta_args &a = p.a;
     const dim3 grid((unsigned)(a.nheads * ((a.headdim + kRows - 1) / kRows)), (unsigned)(a.cu_seqlens ? a.nseqs : a.batch));
-    const size_t smem = (size_t)(2 * kTok * NE * L + kTok * kRows + 2 * kTok) * 4;
-    cudaError_t e = set_smem(delta_scan_kernel<T, NE, L, W>, smem);
+    const size_t smem = (size_t)scan_floats<NE, L, W, Y>() * 4;
+    cudaError_t e = set_smem(delta_scan_kernel<T, NE, L, W, Y>, smem);
     if (e != cudaSuccess) return e;
-    delta_scan_kernel<T, NE, L, W><<<grid, W * 32, smem, st>>>(p);
+    delta_scan_kernel<T, NE, L, W, Y><<<grid, W * 32, smem, st>>>(p);
     return cudaGetLastError();
+}
+template <typename T, int NE, int L, int W>
+cudaError_t run_fwd(const Args &p, cudaStream_t st) {
+    return p.a.y ? run_scan<T, NE, L, W, true>(p, st) : run_scan<T, NE, L, W, false>(p, st);
 }
 template <typename T, int NE, int TR, int L, int W>
 cudaError_t run_bwd(const BwdArgs &p, cudaStream_t st) {
@@ -747,7 +770,7 @@ template <typename T>
 cudaError_t pick_fwd(const Args &p, cudaStream_t st) {
     const int64_t N = p.a.dstate;
     if (few_rows(p.a) && N <= 64) return run_fwd<T, 4, 16, 4>(p, st);
-    if (few_rows(p.a)) return N <= 128 ? run_fwd<T, 4, 32, 4>(p, st) : run_fwd<T, 8, 32, 4>(p, st);
+    if (few_rows(p.a)) return N <= 128 ? run_fwd<T, 8, 16, 4>(p, st) : run_fwd<T, 8, 32, 4>(p, st);
     if (N <= 32) return run_fwd<T, 4, 8, 8>(p, st);
     if (N <= 64) return run_fwd<T, 8, 8, 8>(p, st);
     if (N <= 96) return run_fwd<T, 12, 8, 8>(p, st);
