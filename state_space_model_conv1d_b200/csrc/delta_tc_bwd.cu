@@ -766,13 +766,25 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
                 tc::mma_commit(&ax.done);
             }
             __syncwarp();
-            for (int x = tid; x < ns * (int)(L::kAtoms * kTile / 16); x += kGradThreads) {
-                const uint8_t *t = sm + L::REC + x / (L::kAtoms * kTile / 16) * L::rec + x % (L::kAtoms * kTile / 16) * 16;
-                float u[8], v[8];
-                tc::unpack_bf16x8(*reinterpret_cast<const uint4 *>(t), u);
-                tc::unpack_bf16x8(*reinterpret_cast<const uint4 *>(t + L::kAtoms * kTile), v);
+            for (int x = 0; x < ns; ++x) {
+                constexpr int kPer = L::kAtoms * kTile / 16 / kGradThreads;
+                uint4 hv[kPer], dv[kPer];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) hd = fmaf(u[e], v[e], hd);
+                for (int y = 0; y < kPer; ++y) {
+                    const uint8_t *t = sm + L::REC + x * L::rec + (tid + y * kGradThreads) * 16;
+                    hv[y] = *reinterpret_cast<const uint4 *>(t);
+                    dv[y] = *reinterpret_cast<const uint4 *>(t + L::kAtoms * kTile);
+                }
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int y = 0; y < kPer; ++y) {
+                    float u[8], v[8];
+                    tc::unpack_bf16x8(hv[y], u);
+                    tc::unpack_bf16x8(dv[y], v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) part[e & 3] = fmaf(u[e], v[e], part[e & 3]);
+                }
+                hd += (part[0] + part[1]) + (part[2] + part[3]);
             }
             done();
             if (!__syncthreads_and(ok)) {              // the tiles are read and used
@@ -793,13 +805,20 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
         {
             const int j0 = 32 * cf;
             const float ci = ax.tab.cs[i], f = upper ? -ax.tab.beta[i] : a.scale;
+            float cj[32], own_x = 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                const float4 c4 = *reinterpret_cast<const float4 *>(ax.tab.cs + j0 + e);
+                cj[e] = c4.x; cj[e + 1] = c4.y; cj[e + 2] = c4.z; cj[e + 3] = c4.w;
+            }
             tc::tmem_ld32(tl + TG_U + j0, x);
+            const int last = i < nt ? (upper ? i - 1 : i) - j0 : -1;   // columns up to it count
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-                const int j = j0 + e;
-                if (upper && j == i) ax.ru[i] = x[e];
-                x[e] = (upper ? j < i : j <= i) && i < nt ? f * ex2(ci - ax.tab.cs[j]) * x[e] : 0.f;
+                if (e == i - j0) own_x = x[e];
+                x[e] = e <= last ? f * ex2(ci - cj[e]) * x[e] : 0.f;
             }
+            if (upper && (unsigned)(i - j0) < 32u) ax.ru[i] = own_x;
             uint8_t *row = sm + L::A + 2 * kTile;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -909,15 +928,25 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
         }
         __syncthreads();
     }
-    if (ok && i < nt) {
-        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(upper ? p.b.dk : p.b.dq) +
-                           ((blk.row * a.seqlen + blk.t0 + i) * a.ngroups + grp) * N + cf * (NK / 2);
+    // dq and dk by way of the matrix's place: a lane's own row would take a line per store.  16-byte pieces, those of
+    // neighbouring rows in different banks.
+    if (__syncthreads_and(ok)) {
+        constexpr int kRow = NK / 8;
 #pragma unroll
         for (int k = 0; k < NK / 16; ++k)
-            if (cf * (NK / 2) + 8 * k < N)
-                *reinterpret_cast<uint4 *>(o + 8 * k) =
-                    make_uint4(pack2(acc[8 * k], acc[8 * k + 1]), pack2(acc[8 * k + 2], acc[8 * k + 3]),
-                               pack2(acc[8 * k + 4], acc[8 * k + 5]), pack2(acc[8 * k + 6], acc[8 * k + 7]));
+            *reinterpret_cast<uint4 *>(sm + L::A + (r * kRow + ((cf * (NK / 16) + k) ^ (r & 7))) * 16) =
+                make_uint4(pack2(acc[8 * k], acc[8 * k + 1]), pack2(acc[8 * k + 2], acc[8 * k + 3]),
+                           pack2(acc[8 * k + 4], acc[8 * k + 5]), pack2(acc[8 * k + 6], acc[8 * k + 7]));
+        __syncthreads();
+#pragma unroll
+        for (int y = 0; y < 128 * kRow / kGradThreads; ++y) {
+            const int x = tid + y * kGradThreads, row = x / kRow, c = x % kRow;
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(row >= 64 ? p.b.dk : p.b.dq) +
+                               ((blk.row * a.seqlen + blk.t0 + (row & 63)) * a.ngroups + grp) * N + c * 8;
+            if ((row & 63) < nt && c * 8 < N)
+                *reinterpret_cast<uint4 *>(o) =
+                    *reinterpret_cast<const uint4 *>(sm + L::A + (row * kRow + (c ^ (row & 7))) * 16);
+        }
     }
     if (!ok && tid == 0) {
         // a wait ran out: what is in flight lands before the CTA ends
