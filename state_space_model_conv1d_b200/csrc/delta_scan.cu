@@ -5,28 +5,29 @@
 //     w = a_t h,  s = w . k_t,  u = beta_t (v_t[p] - s),  h = w + u k_t,
 //     y_t[p] = scale (h . q_t) = scale (w . q_t + u (k_t . q_t)),
 // so rows are spread over lanes: 8 lanes hold one row (4 consecutive states
-// of every 32) and a warp 4 rows, or a warp one row.  The dot products of a
-// token are summed in one pass of shuffles.  The chain over the tokens bounds
-// the time, not memory; a sequence's rows run in separate CTAs.
+// of every 32) and a warp 4 rows, or 16 or 32 lanes a row where rows are few.
+// The dot product that the chain waits for is summed in one pass of shuffles.
+// The chain over the tokens bounds the time (about 170 ns a token), not memory;
+// a sequence's rows run in separate CTAs.  2 x 333 tokens, 6 heads, P 40, N 72,
+// fp32: 57 us (2.7 MB, 0.4 us of HBM); the gradients of 5 packed sequences of
+// 517 tokens, 4 heads, P 48, N 64: 32 us for the checkpoints, 115 us backwards
+// and 6 us for the sums.
 //
 // Backward, per row, from the last token to the first, with d = dL/dh_t:
 //     d += scale dy q;  du = d . k;  dv = beta du;  ds = -beta du;
 //     dbeta = sum_p du (v - s);  dq = scale sum_p dy h_t;
 //     dk = sum_p (u d + ds w);  d += ds k;  dg = sum_{p,n} d w;  d = a d.
 // The states before every 32nd token are kept by a forward pass; the tokens
-// between are recomputed in runs that fit in registers.  Each CTA owns some
-// rows and writes their share of dq, dk, dg, dbeta; a second kernel adds the shares
-// in a fixed order.
+// between are recomputed, in runs that fit in registers or, with few rows, once
+// into shared memory.  Each CTA owns some rows and writes their share of dq,
+// dk, dg, dbeta; a last kernel adds the shares in a fixed order.
 #include "common.cuh"
 #include "delta.h"
 
 namespace ssm {
 namespace {
 
-// L lanes per state row and W warps per CTA: 8 and 8 (32 rows per CTA), or, where
-// that gives a scheduler less than a warp, 32 and 4 (4 rows): the chain over the
-// tokens is latency, and a quarter of the states per lane is a third of the
-// instructions of a token.
+// L lanes per state row, W warps per CTA.
 template <int L, int W> struct Cut {
     static constexpr int threads = W * 32, rows = W * 32 / L, per_warp = 32 / L;
 };
@@ -760,11 +761,20 @@ cudaError_t run_rows_bwd(const BwdArgs &p, cudaStream_t st) {
 }
 
 int64_t seqs_of(const ssm_delta_args &a) { return a.cu_seqlens ? a.nseqs : a.batch; }
-// Few rows: with 4 of them a warp, less than a warp for each of the GPU's schedulers.
-bool few_rows(const ssm_delta_args &a) { return seqs_of(a) * a.nheads * a.headdim < 4LL * 4 * sm_count(); }
-int64_t slices_of(const ssm_delta_args &a) {
-    const int rows = !few_rows(a) ? Cut<8, 8>::rows : a.dstate <= 64 ? Cut<16, 4>::rows : Cut<32, 4>::rows;
+// Few rows: CTAs of 4 warps with a row in 16 (dstate <= 64) or 32 lanes fit on the
+// SMs at once.  The chain is latency there, and a quarter of the states per lane
+// shortens a token; with more rows the shuffles and copies of k and q cost more
+// than that gains.  Forward / backward in us, few-row form against the other:
+// 2 x 333 tokens, 6 heads, P 40, N 72 (480 rows) 62 / 245 against 82 / 400;
+// 2 x 512, 16 heads, P 64, N 64 (2048 rows) 96 / 556 against 96 / 470;
+// 4 x 256, 16 heads, P 64, N 64 (4096 rows) 68 / 536 against 53 / 247.
+int64_t few_slices(const ssm_delta_args &a) {
+    const int rows = a.dstate <= 64 ? Cut<16, 4>::rows : Cut<32, 4>::rows;
     return (a.headdim + rows - 1) / rows;
+}
+bool few_rows(const ssm_delta_args &a) { return seqs_of(a) * a.nheads * few_slices(a) <= sm_count(); }
+int64_t slices_of(const ssm_delta_args &a) {
+    return few_rows(a) ? few_slices(a) : (a.headdim + Cut<8, 8>::rows - 1) / Cut<8, 8>::rows;
 }
 template <typename T>
 cudaError_t pick_fwd(const Args &p, cudaStream_t st) {

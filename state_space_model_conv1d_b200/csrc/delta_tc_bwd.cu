@@ -26,6 +26,11 @@
 // Rounding: on the way to dh0 every factor that is not exact goes as two bf16
 // parts (as in the forward); what ends in a bf16 gradient is rounded to bf16
 // once per factor.
+//
+// 4 x 2048 tokens, 16 heads of P 128 in 8 groups, N 128: pre-pass 52 us, states'
+// pass 119, gradients' chain 155 (both chains' latency: 64 CTAs, 32 blocks each),
+// the blocks' gradients 124 (230 MB of kept operands; one CTA an SM, whose
+// products, passes and loads follow one another, 14k cycles a head).
 #include <string.h>
 
 #include "delta_tc.cuh"
