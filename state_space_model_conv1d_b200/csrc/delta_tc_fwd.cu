@@ -20,8 +20,8 @@
 // to bf16 once, like y itself.
 //
 // Roles: 8 warps for the chain (two per lane quarter, half of the columns
-// each), 4 for the output, one thread for the MMAs and one warp for the loads
-// and the gate tables.  A block costs three
+// each), 4 for the output (one thread of them issues its product), one thread
+// for the chain's MMAs and one warp for the loads and the gate tables.  A block costs three
 // dependent groups of MMAs (h k with h q beside it, T R, the state's update)
 // with a pass over registers between them; each pass hands over its first half
 // as soon as it is written, so that the MMAs of that half overlap the second.
@@ -64,7 +64,7 @@ enum Bar {
     B_FULL0, B_FULL1, B_EMPTY0, B_EMPTY1, B_TAB0, B_TAB1,
     B_H0, B_H1, B_M1, B_R0, B_R1, B_M2, B_U0, B_U1, B_UOP, B_M3,    // the chain (halves 0 and 1 of a pass)
     B_HQ, B_M5,                                                     // the output
-    B_DRAIN, B_COUNT
+    B_DRAIN, B_DRAIN2, B_COUNT
 };
 
 // Operand columns of the state's part (0 high, 1 low): states 32 b .. 32 b + 31 of column half cf.
@@ -153,12 +153,12 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
     const int64_t slot0 = seq_slot(a.cu_seqlens, s, p.nblk);
     if (warp == 0) tc::tmem_alloc(&ax.tmem, kTmemCols);
     if (tid == 0) {
-        constexpr int kEmpty = 1 + kChainWarps + (ST ? 0 : kOutWarps);
+        constexpr int kEmpty = 1 + kChainWarps + (ST ? 0 : 1 + kOutWarps);
         constexpr int counts[B_COUNT] = {
             1, 1, kEmpty, kEmpty, 1, 1,
             kChainWarps, kChainWarps, 1, kChainWarps, kChainWarps, 1, kChainWarps, kChainWarps, kChainWarps, 1,
             kOutWarps, 1,
-            1};
+            1, 1};
         for (int i = 0; i < B_COUNT; ++i) tc::mbar_init(&ax.mb[i], counts[i]);
         tc::mbar_init_fence();
         ax.abort = 0;
@@ -386,6 +386,29 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
                 arrive(&ax.mb[B_HQ]);
                 arrive(&ax.mb[B_EMPTY0 + stg]);
             }
+            // attention x u, issued here: in the MMA warp its waits would queue up behind the chain's products
+            if (q == 0) {
+                ok = ok && wait(B_FULL0 + stg, (c >> 1) & 1) && wait(B_HQ, ph) && wait(B_UOP, ph);
+                if (ok && lane == 0) {
+                    tc::fence_after_sync();
+                    constexpr uint32_t ID5 = tc::idesc_bf16(128, 64, 0, 0);
+                    const uint64_t dP = tc::desc_sw128(sb + stg * L::stage + L::PM, 16, 1024);
+#pragma unroll
+                    for (int hh = 0; hh < (DUAL ? 2 : 1); ++hh)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint32_t A = tm + TM_RU + (kk >> 1) * 32 + (kk & 1) * 8;
+                            const uint64_t B = dP + hh * (kTile >> 4) + kk * 2;
+                            if constexpr (DUAL)
+                                mma_ts_lanes(tm + TM_O, A, B, ID5, 1, hh ? ~0u : 0u, hh ? 0u : ~0u);
+                            else
+                                mma_ts(tm + TM_O, A, B, ID5, 1);
+                        }
+                    tc::mma_commit(&ax.mb[B_M5]);
+                    tc::mma_commit(&ax.mb[B_EMPTY0 + stg]);
+                }
+                __syncwarp();
+            }
             ok = ok && wait(B_M5, ph);
             tc::fence_after_sync();
             // y by way of shared memory: whole 16-byte pieces of token rows
@@ -411,17 +434,16 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------------ MMAs
         constexpr uint32_t ID1 = tc::idesc_bf16(128, 128, 0, 0), ID2 = tc::idesc_bf16(128, DUAL ? 128 : 64, 0, 0),
-                           ID3 = tc::idesc_bf16(128, NK, 0, 1), ID5 = tc::idesc_bf16(128, 64, 0, 0);
+                           ID3 = tc::idesc_bf16(128, NK, 0, 1);
         bool ok = true;
         for (int c = 0; c < n && ok; ++c) {
             const uint32_t ph = c & 1;
             const int stg = c & 1;
             const uint32_t st = sb + stg * L::stage;
             const uint64_t dK = tc::desc_sw128(st + L::K, 16, 1024), dKm = tc::desc_sw128(st + L::K, 2 * kTile, 1024);
-            const uint64_t dT = tc::desc_sw128(st + L::T, 16, 1024), dP = tc::desc_sw128(st + L::PM, 16, 1024);
-            // h k and h q, once the last block's output has read h q and used u
-            ok = wait(B_FULL0 + stg, (c >> 1) & 1) &&
-                 (ST || c == 0 || (wait(B_HQ, ph ^ 1) && wait(B_M5, ph ^ 1)));
+            const uint64_t dT = tc::desc_sw128(st + L::T, 16, 1024);
+            // h k and h q, once the last block's attention product has used u (it follows the reading of h q)
+            ok = wait(B_FULL0 + stg, (c >> 1) & 1) && (ST || c == 0 || wait(B_M5, ph ^ 1));
 #pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 ok = ok && wait(B_H0 + b, ph);
@@ -472,32 +494,11 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
                             mma_ts(tm + TM_H, tm + TM_OP + part * 32 + kk * 8, dKm + kk * 128, ID3, 1);
                     if (b) {
                         tc::mma_commit(&ax.mb[B_M3]);
-                        if (ST) tc::mma_commit(&ax.mb[B_EMPTY0 + stg]);
+                        tc::mma_commit(&ax.mb[B_EMPTY0 + stg]);
                     }
                 }
                 __syncwarp();
             }
-            if (ST) continue;
-            // attention x u
-            ok = ok && wait(B_UOP, ph) && wait(B_HQ, ph);
-            if (!ok) break;
-            tc::fence_after_sync();
-            if (lane == 0) {
-#pragma unroll
-                for (int hh = 0; hh < (DUAL ? 2 : 1); ++hh)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t A = tm + TM_RU + (kk >> 1) * 32 + (kk & 1) * 8;
-                        const uint64_t B = dP + hh * (kTile >> 4) + kk * 2;
-                        if constexpr (DUAL)
-                            mma_ts_lanes(tm + TM_O, A, B, ID5, 1, hh ? ~0u : 0u, hh ? 0u : ~0u);
-                        else
-                            mma_ts(tm + TM_O, A, B, ID5, 1);
-                    }
-                tc::mma_commit(&ax.mb[B_M5]);
-                tc::mma_commit(&ax.mb[B_EMPTY0 + stg]);
-            }
-            __syncwarp();
         }
     } else {
         // --------------------------------------------------- loads and gate tables
@@ -565,10 +566,11 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
         if (*ab && lane == 0)                  // copies in flight land before the CTA ends
             for (int c = max(0, issued - 2); c < issued; ++c) tc::mbar_wait(&ax.mb[B_FULL0 + (c & 1)], (c >> 1) & 1, 1u << 22);
     }
-    if (*ab && lane == 0 && warp == kMmaWarp) {
+    if (*ab && lane == 0 && (warp == kMmaWarp || warp == kOut0)) {
         // after a wait that ran out: the MMAs in flight complete before tensor memory is freed
-        tc::mma_commit(&ax.mb[B_DRAIN]);
-        tc::mbar_wait(&ax.mb[B_DRAIN], 0, 1u << 22);
+        const int b = warp == kMmaWarp ? B_DRAIN : B_DRAIN2;
+        tc::mma_commit(&ax.mb[b]);
+        tc::mbar_wait(&ax.mb[b], 0, 1u << 22);
     }
     __syncwarp();
     tc::fence_before_sync();
