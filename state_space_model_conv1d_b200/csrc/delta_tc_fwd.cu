@@ -30,11 +30,13 @@
 // the other and make one operand of 128 rows, and so do the two T of a CTA
 // whose halves are different heads.
 //
-// 4 x 4096 tokens, 32 heads of P 128, N 128: 257 us, 64 blocks one after the
-// other in 128 CTAs, 4 us (7.2k cycles) a block: the chain's latency, three
-// waits on MMAs of 500 to 1500 cycles and the passes between them; the tensor
-// pipe has work for a third of it.  With two heads of P 64 in a CTA a block takes
-// 8k cycles.  The token-by-token form takes 15 times as long on this call.
+// 4 x 4096 tokens, 32 heads of P 128, N 128: 237 us, 64 blocks one after the
+// other in 128 CTAs, 3.7 us (6.7k cycles) a block: the chain's latency, 36 MMAs
+// of about 100 cycles and the passes between them.  28301 packed tokens, 64 heads
+// of P 64, two of them in a CTA: 437 us, 7.1k cycles a block.  (With the output's
+// product in the MMA warp, whose waits then queue up behind the products already
+// issued, it was 257 and 472 us.)  The token-by-token form takes 15 times as long
+// on the first call.
 #include <string.h>
 
 #include "delta_tc.cuh"
