@@ -60,7 +60,7 @@ struct PrepSmem {
         Head head[kPair];
     };
     Gates gates[kPair];
-    uint64_t mb;
+    uint64_t full, done;                   // K and Q are here, their products are made: one phase each
     uint32_t tmem;
     int abort;
 };
@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     if (w == 0) tc::tmem_alloc(&sm.tmem, 64);
     if (tid == 0) {
-        tc::mbar_init(&sm.mb, 1);
+        tc::mbar_init(&sm.full, 1);
+        tc::mbar_init(&sm.done, 1);
         tc::mbar_init_fence();
         sm.abort = 0;
     }
@@ -242,13 +243,13 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
     bool ok = true;
     if (tid == 0) {
         // rows behind the sequence's end may hold anything: a product only meets its own two rows
-        tc::mbar_expect_tx(&sm.mb, NK / 64 * 2 * kTile);
+        tc::mbar_expect_tx(&sm.full, NK / 64 * 2 * kTile);
 #pragma unroll
         for (int x = 0; x < NK / 64; ++x) {
-            tma_load_4d(sm.kq + x * 2 * kTile, &tm_k, 64 * x, grp, (int)b.t0, (int)b.row, &sm.mb);
-            tma_load_4d(sm.kq + x * 2 * kTile + kTile, &tm_q, 64 * x, grp, (int)b.t0, (int)b.row, &sm.mb);
+            tma_load_4d(sm.kq + x * 2 * kTile, &tm_k, 64 * x, grp, (int)b.t0, (int)b.row, &sm.full);
+            tma_load_4d(sm.kq + x * 2 * kTile + kTile, &tm_q, 64 * x, grp, (int)b.t0, (int)b.row, &sm.full);
         }
-        ok = wait_bar(&sm.mb, &sm.abort, 0, p.err);
+        ok = wait_bar(&sm.full, &sm.abort, 0, p.err);
         tc::fence_after_sync();
         const uint64_t d = tc::desc_sw128(tc::smem_u32(sm.kq), 16, 1024);
 #pragma unroll
@@ -256,11 +257,9 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
             const uint32_t o = ((kk >> 2) * 2 * kTile + (kk & 3) * 32) >> 4;
             tc::mma_bf16(tm, d + o, d + o, tc::idesc_bf16(128, 64, 0, 0), kk > 0);
         }
-        tc::mma_commit(&sm.mb);
+        tc::mma_commit(&sm.done);
     }
     __syncwarp();
-    ok = wait_bar(&sm.mb, &sm.abort, 1, p.err) && ok;
-    tc::fence_after_sync();
     const uint32_t tl = tm + ((uint32_t)(32 * w) << 16);
     const int64_t hbytes = p.bwd ? kHeadBytesBwd : kHeadBytes;
     const int i = (w & 1) * 32 + lane;                 // this thread's row of K K^T (warps 0, 1) or Q K^T (2, 3)
@@ -285,6 +284,10 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
             gt.lo[lane + 32] = (float)(c1 - (double)(float)c1);
             gt.beta[lane] = b0;
             gt.beta[lane + 32] = b1;
+        }
+        if (hb == 0) {                                 // the products were made meanwhile
+            ok = wait_bar(&sm.done, &sm.abort, 0, p.err) && ok;
+            tc::fence_after_sync();
         }
         if (!__syncthreads_and(ok)) break;             // (the error word is set; nothing was computed)
         for (int hh = 0; hh < nh; ++hh) {
@@ -359,6 +362,11 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
         }
         __syncthreads();
     }
+    if (!ok && tid == 0) {                             // a wait ran out: what is in flight lands before the CTA ends
+        tc::mbar_wait(&sm.full, 0, 1u << 22);
+        tc::mbar_wait(&sm.done, 0, 1u << 22);
+    }
+    __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     if (w == 0) {
