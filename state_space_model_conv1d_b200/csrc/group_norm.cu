@@ -8,7 +8,7 @@
 // contiguous stretch.  A unit stays with its group, which keeps the weights
 // (forward) and their gradients' sums (backward) in registers over its tokens.
 // Groups of 512, gate behind the norm: 402 MB in 75 us, 5.4 TB/s; groups of 64
-// with the gate in front, backward: 671 MB in 141 us, 4.8 TB/s.  Past 4096
+// with the gate in front, backward: 671 MB in 141 us, 4.8 TB/s.  Past 8192
 // channels a group the backward's registers spill.
 //
 // Backward, with n the normalised values, t = n w + bias, dt = dL/dt, dn = dt w:
@@ -239,8 +239,9 @@ __global__ void __launch_bounds__(threads_of<TPU>()) group_norm_kernel(const Arg
     }
 }
 
+// (one vector per thread: two CTAs an SM and at most 128 registers; more vectors: all that a thread can have)
 template <typename T, int TPU, int VPT, bool VEC, Kind K>
-__global__ void __launch_bounds__(threads_of<TPU>()) group_norm_bwd_kernel(const Args p) {
+__global__ void __launch_bounds__(threads_of<TPU>(), VPT == 1 ? 2 : 1) group_norm_bwd_kernel(const Args p) {
     __shared__ float red[threads_of<TPU>() / 32 * 2];
     const ssm_norm_args &a = p.a;
     constexpr int UPB = threads_of<TPU>() / TPU;
@@ -280,8 +281,8 @@ __global__ void __launch_bounds__(threads_of<TPU>()) group_norm_bwd_kernel(const
         const bool live = first < p.splits && row < p.rows;
         if (TPU <= 32 && __all_sync(~0u, !live)) break;
         Raw<T, VPT> xn, zn, gn;
-        // with one vector per thread there are registers for the next token's loads
-        if (VPT == 1 && it + 1 < turns) fetch(it + 1, xn, zn, gn);
+        // with up to two vectors per thread there are registers for the next token's loads
+        if (VPT <= 2 && it + 1 < turns) fetch(it + 1, xn, zn, gn);
         float s[VPT][8], sg[K == kNoGate ? 1 : VPT][8], dn[VPT][8];
         float dz[K == kGate ? VPT : 1][8];
 #pragma unroll
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(threads_of<TPU>()) group_norm_bwd_kernel(const
                 if (K != kNoGate) store<T, TPU, VPT, VEC>((T *)p.dz + row * a.channels + c0, o2, th, i, D);
             }
         }
-        if (VPT == 1) {
+        if (VPT <= 2) {
             x = xn;
             z = zn;
             g = gn;
@@ -391,35 +392,39 @@ __global__ void __launch_bounds__(256) norm_shares_kernel(const float *pw, const
 
 // Threads per unit and 8-channel vectors per thread for a group of D channels:
 // the narrowest unit that holds the group, so that few lanes idle (fewer shapes
-// without 16-byte accesses, where the loads cost more than idle lanes).  Gated
-// forward / backward of 16384 rows of 4096 bf16 channels in us, this shape
-// against the next wider one: D 64 79 / 133 against 295 / 468, D 128 77 / 134
-// against 153 / 243, D 512 75 / 199 against 125 / 267, D 2048 80 / 251 against
-// 112 / 379.
+// without 16-byte accesses, where the loads cost more than idle lanes); in the
+// backward, which holds four times as much, D 2048 in single vectors.  Gated
+// forward / backward of 16384 rows of 4096 bf16 channels in us, and with another
+// shape: D 64 79 / 133 (units of 32 threads 295 / 468), D 128 77 / 134 (153 / 243),
+// D 512 74 / 140 (64 threads of one vector 81 / 151, 128 threads 125 / 267), D 2048
+// 79 / 155 (forward as the backward 83, backward as the forward 179), D 4096
+// 79 / 160 (512 threads of one vector 90 / 173); rows of one group of 8192: 159 / 490
+// (four vectors 342 / 1637).
 struct Shape {
     int tpu, vpt;
 };
-Shape shape_of(int64_t D, bool vec) {
+Shape shape_of(int64_t D, bool vec, bool bwd) {
     if (vec && D <= 64) return {8, 1};
     if (vec && D <= 128) return {16, 1};
     if (D <= 256) return {32, 1};
     if (vec && D <= 512) return {32, 2};
     if (D <= 1024) return {128, 1};
-    if (vec && D <= 2048) return {128, 2};
+    if (vec && D <= 2048) return bwd ? Shape{256, 1} : Shape{128, 2};
     if (D <= 4096) return {256, 2};
+    if (vec && D <= 8192) return {512, 2};
     return {512, 4};
 }
 
-// Units per group: as many as fill the GPU at `warps` warps per SM, so that a
+// Units per group: as many as fill the GPU at so many warps per SM, so that a
 // unit keeps its weights over many tokens.
-int splits_of(const ssm_norm_args &a, bool vec, int warps) {
-    const Shape s = shape_of(a.channels / a.groups, vec);
-    const int64_t rows = a.batch * a.seqlen, units = (int64_t)sm_count() * warps * 32 / s.tpu;
+constexpr int kFwdWarps = 32, kBwdWarps = 16;
+int splits_of(const ssm_norm_args &a, bool vec, bool bwd) {
+    const Shape s = shape_of(a.channels / a.groups, vec, bwd);
+    const int64_t rows = a.batch * a.seqlen, units = (int64_t)sm_count() * (bwd ? kBwdWarps : kFwdWarps) * 32 / s.tpu;
     int64_t n = units / a.groups;
     if (n < 1) n = 1;
     return (int)(n < rows ? n : rows);
 }
-constexpr int kFwdWarps = 32, kBwdWarps = 16;
 
 template <bool BWD, typename T, int TPU, int VPT, bool VEC, Kind K>
 void run(const Args &p, cudaStream_t st) {
@@ -431,15 +436,16 @@ void run(const Args &p, cudaStream_t st) {
 }
 template <bool BWD, typename T, Kind K>
 void pick(const Args &p, bool vec, cudaStream_t st) {
-    const Shape s = shape_of(p.a.channels / p.a.groups, vec);
+    const Shape s = shape_of(p.a.channels / p.a.groups, vec, BWD);
     if (vec) {
         if (s.tpu == 8) run<BWD, T, 8, 1, true, K>(p, st);
         else if (s.tpu == 16) run<BWD, T, 16, 1, true, K>(p, st);
         else if (s.tpu == 32 && s.vpt == 1) run<BWD, T, 32, 1, true, K>(p, st);
         else if (s.tpu == 32) run<BWD, T, 32, 2, true, K>(p, st);
         else if (s.tpu == 128 && s.vpt == 1) run<BWD, T, 128, 1, true, K>(p, st);
-        else if (s.tpu == 128) run<BWD, T, 128, 2, true, K>(p, st);
+        else if (s.tpu == 128 || (s.tpu == 256 && s.vpt == 1)) run<BWD, T, BWD ? 256 : 128, BWD ? 1 : 2, true, K>(p, st);
         else if (s.tpu == 256) run<BWD, T, 256, 2, true, K>(p, st);
+        else if (s.vpt == 2) run<BWD, T, 512, 2, true, K>(p, st);
         else run<BWD, T, 512, 4, true, K>(p, st);
     } else {
         if (s.tpu == 32) run<BWD, T, 32, 1, false, K>(p, st);
@@ -476,7 +482,7 @@ cudaError_t launch_group_norm(const ssm_norm_args &a, cudaStream_t st) {
     const bool vec = (a.channels / a.groups) % 8 == 0 && vec_ok(a.x, a.x_batch_stride, a.x_token_stride, es) &&
                      vec_ok(a.z, a.z_batch_stride, a.z_token_stride, es) &&
                      vec_ok(a.y, a.y_batch_stride, a.y_token_stride, es);
-    p.splits = splits_of(a, vec, kFwdWarps);
+    p.splits = splits_of(a, vec, false);
     return launch<false>(p, vec, st);
 }
 
@@ -484,7 +490,7 @@ size_t group_norm_bwd_workspace_bytes(const ssm_norm_bwd_args &b) {
     const ssm_norm_args &a = b.fwd;
     if (a.batch * a.seqlen == 0) return 0;
     // shapes alone decide the size: room for the layout with more units per group
-    const int n = splits_of(a, true, kBwdWarps), m = splits_of(a, false, kBwdWarps);
+    const int n = splits_of(a, true, true), m = splits_of(a, false, true);
     return 2 * (((size_t)(n > m ? n : m) * a.channels * 4 + 255) / 256 * 256);
 }
 
@@ -513,7 +519,7 @@ cudaError_t launch_group_norm_bwd(const ssm_norm_bwd_args &b, void *ws, cudaStre
                      vec_ok(a.z, a.z_batch_stride, a.z_token_stride, es) &&
                      vec_ok(b.dy, b.dy_batch_stride, b.dy_token_stride, es) && vec_ok(b.dx, 0, 0, es) &&
                      vec_ok(b.dz, 0, 0, es);
-    p.splits = splits_of(a, vec, kBwdWarps);
+    p.splits = splits_of(a, vec, true);
     cudaError_t e = launch<true>(p, vec, st);
     if (e != cudaSuccess || !p.pw) return e;
     norm_shares_kernel<<<(unsigned)((a.channels + 31) / 32), 256, 0, st>>>(p.pw, p.pb, p.splits, a.channels, b.dweight,
