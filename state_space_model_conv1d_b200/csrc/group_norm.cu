@@ -391,28 +391,29 @@ __global__ void __launch_bounds__(256) norm_shares_kernel(const float *pw, const
 }
 
 // Threads per unit and 8-channel vectors per thread for a group of D channels:
-// the narrowest unit that holds the group, so that few lanes idle (fewer shapes
-// without 16-byte accesses, where the loads cost more than idle lanes); in the
-// backward, which holds four times as much, D 2048 in single vectors.  Gated
+// the narrowest unit that holds the group, so that few lanes idle; in the backward,
+// which holds four times as much, and without 16-byte accesses in single vectors
+// where those do not cost a wider unit.  Gated
 // forward / backward of 16384 rows of 4096 bf16 channels in us, and with another
 // shape: D 64 79 / 133 (units of 32 threads 295 / 468), D 128 77 / 134 (153 / 243),
 // D 512 74 / 140 (64 threads of one vector 81 / 151, 128 threads 125 / 267), D 2048
 // 79 / 155 (forward as the backward 83, backward as the forward 179), D 4096
 // 79 / 160 (512 threads of one vector 90 / 173); rows of one group of 8192: 159 / 490
-// (four vectors 342 / 1637).
+// (four vectors 342 / 1637).  Without 16-byte accesses D 63 132 / 218 (32 threads
+// 374 / 645), D 511 140 / 225 (128 threads 249 / 404), D 2047 117 / 234 (two vectors
+// 268 / 596).
 struct Shape {
     int tpu, vpt;
 };
 Shape shape_of(int64_t D, bool vec, bool bwd) {
-    if (vec && D <= 64) return {8, 1};
-    if (vec && D <= 128) return {16, 1};
+    if (D <= 64) return {8, 1};
+    if (D <= 128) return {16, 1};
     if (D <= 256) return {32, 1};
-    if (vec && D <= 512) return {32, 2};
+    if (D <= 512) return vec ? Shape{32, 2} : Shape{64, 1};
     if (D <= 1024) return {128, 1};
-    if (vec && D <= 2048) return bwd ? Shape{256, 1} : Shape{128, 2};
+    if (D <= 2048) return vec && !bwd ? Shape{128, 2} : Shape{256, 1};
     if (D <= 4096) return {256, 2};
-    if (vec && D <= 8192) return {512, 2};
-    return {512, 4};
+    return D <= 8192 ? Shape{512, 2} : Shape{512, 4};
 }
 
 // Units per group: as many as fill the GPU at so many warps per SM, so that a
@@ -434,25 +435,24 @@ void run(const Args &p, cudaStream_t st) {
     if constexpr (BWD) group_norm_bwd_kernel<T, TPU, VPT, VEC, K><<<grid, threads_of<TPU>(), 0, st>>>(p);
     else group_norm_kernel<T, TPU, VPT, VEC, K><<<grid, threads_of<TPU>(), 0, st>>>(p);
 }
+template <bool BWD, typename T, bool VEC, Kind K>
+void with(const Args &p, Shape s, cudaStream_t st) {
+    if (s.tpu == 8) run<BWD, T, 8, 1, VEC, K>(p, st);
+    else if (s.tpu == 16) run<BWD, T, 16, 1, VEC, K>(p, st);
+    else if (s.tpu == 32 && s.vpt == 1) run<BWD, T, 32, 1, VEC, K>(p, st);
+    else if (s.tpu == 128 && s.vpt == 1) run<BWD, T, 128, 1, VEC, K>(p, st);
+    else if (s.tpu == 32 || s.tpu == 64) run<BWD, T, VEC ? 32 : 64, VEC ? 2 : 1, VEC, K>(p, st);
+    else if (s.tpu == 128 || (s.tpu == 256 && s.vpt == 1))
+        run<BWD, T, VEC && !BWD ? 128 : 256, VEC && !BWD ? 2 : 1, VEC, K>(p, st);
+    else if (s.tpu == 256) run<BWD, T, 256, 2, VEC, K>(p, st);
+    else if (s.vpt == 2) run<BWD, T, 512, 2, VEC, K>(p, st);
+    else run<BWD, T, 512, 4, VEC, K>(p, st);
+}
 template <bool BWD, typename T, Kind K>
 void pick(const Args &p, bool vec, cudaStream_t st) {
     const Shape s = shape_of(p.a.channels / p.a.groups, vec, BWD);
-    if (vec) {
-        if (s.tpu == 8) run<BWD, T, 8, 1, true, K>(p, st);
-        else if (s.tpu == 16) run<BWD, T, 16, 1, true, K>(p, st);
-        else if (s.tpu == 32 && s.vpt == 1) run<BWD, T, 32, 1, true, K>(p, st);
-        else if (s.tpu == 32) run<BWD, T, 32, 2, true, K>(p, st);
-        else if (s.tpu == 128 && s.vpt == 1) run<BWD, T, 128, 1, true, K>(p, st);
-        else if (s.tpu == 128 || (s.tpu == 256 && s.vpt == 1)) run<BWD, T, BWD ? 256 : 128, BWD ? 1 : 2, true, K>(p, st);
-        else if (s.tpu == 256) run<BWD, T, 256, 2, true, K>(p, st);
-        else if (s.vpt == 2) run<BWD, T, 512, 2, true, K>(p, st);
-        else run<BWD, T, 512, 4, true, K>(p, st);
-    } else {
-        if (s.tpu == 32) run<BWD, T, 32, 1, false, K>(p, st);
-        else if (s.tpu == 128) run<BWD, T, 128, 1, false, K>(p, st);
-        else if (s.tpu == 256) run<BWD, T, 256, 2, false, K>(p, st);
-        else run<BWD, T, 512, 4, false, K>(p, st);
-    }
+    if (vec) with<BWD, T, true, K>(p, s, st);
+    else with<BWD, T, false, K>(p, s, st);
 }
 template <bool BWD>
 cudaError_t launch(const Args &p, bool vec, cudaStream_t st) {

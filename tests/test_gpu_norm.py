@@ -68,6 +68,13 @@ def test_sizes(dtype, size):
     check(dtype, lead, C, G, "gate", C // G > 1, seed=C)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [40, 63, 104, 127, 333, 504, 777, 1536, 2047, 2048, 3001, 3200, 6000, 7001, 9001])
+def test_group_widths(dtype, D):
+    # every unit's width, with 16-byte accesses and without; more rows than units where rows are cheap
+    check(dtype, (5 if D > 2048 else 150,), 2 * D, 2, "first" if D % 2 else "gate", D % 3 != 0, seed=D)
+
+
 @pytest.mark.parametrize("mean", [False, True])
 @pytest.mark.parametrize("mode", MODES)
 def test_modes(mode, mean):
