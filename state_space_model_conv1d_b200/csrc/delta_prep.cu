@@ -20,8 +20,8 @@
 // and P as bf16, both in the swizzled layout that the chain's operands have.
 // Bound by latency and by shared memory: the inverse reads every row as 16-byte
 // broadcasts, four cycles of return bandwidth each.  4 x 4096 tokens, 32 heads in
-// 16 groups, N 128 (8192 inverses): 127 us for 134 MB read and 201 MB written;
-// 28301 packed tokens, 64 heads of one group (28.8 thousand): 387 us.
+// 16 groups, N 128 (8192 inverses): 129 us for 134 MB read and 201 MB written;
+// 28301 packed tokens, 64 heads of one group (28.8 thousand): 400 us.
 #include <string.h>
 
 #include "delta_tc.cuh"
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
             tma_load_4d(sm.kq + x * 2 * kTile, &tm_k, 64 * x, grp, (int)b.t0, (int)b.row, &sm.full);
             tma_load_4d(sm.kq + x * 2 * kTile + kTile, &tm_q, 64 * x, grp, (int)b.t0, (int)b.row, &sm.full);
         }
-        ok = wait_bar(&sm.full, &sm.abort, 0, p.err);
+        ok = wait_bar(&sm.full, &sm.abort, 0, p.err) || tc::mbar_wait(&sm.full, 0, 1u << 22);
         tc::fence_after_sync();
         const uint64_t d = tc::desc_sw128(tc::smem_u32(sm.kq), 16, 1024);
 #pragma unroll
@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
             gt.beta[lane + 32] = b1;
         }
         if (hb == 0) {                                 // the products were made meanwhile
-            ok = wait_bar(&sm.done, &sm.abort, 0, p.err) && ok;
+            // (after a wait that ran out, one more of a fixed length: what is in flight lands before the CTA ends)
+            ok = (wait_bar(&sm.done, &sm.abort, 0, p.err) || tc::mbar_wait(&sm.done, 0, 1u << 22)) && ok && !sm.abort;
             tc::fence_after_sync();
         }
         if (!__syncthreads_and(ok)) break;             // (the error word is set; nothing was computed)
@@ -362,11 +363,6 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
         }
         __syncthreads();
     }
-    if (!ok && tid == 0) {                             // a wait ran out: what is in flight lands before the CTA ends
-        tc::mbar_wait(&sm.full, 0, 1u << 22);
-        tc::mbar_wait(&sm.done, 0, 1u << 22);
-    }
-    __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     if (w == 0) {
