@@ -152,6 +152,24 @@ def test_two_calls_at_once():
         assert all(torch.equal(a, b) for x, y in zip(want, got) for a, b in zip(x, y))
 
 
+@pytest.mark.parametrize("dtype,P,N", [("f32", 24, 40), ("bf16", 64, 128), ("bf16", 128, 64)])
+def test_state_in_place(dtype, P, N):
+    # h_final may be h0 (empty sequences keep theirs), y of the norm may be x
+    lengths = [70, 0, 1, 130]
+    _, cud = cu_of(lengths)
+    dev, _ = make(15, dtype, 1, sum(lengths), 4, P, 2, N, nseq=len(lengths))
+    x = [dev[n] for n in ("q", "k", "v", "g", "beta")]
+    y, hf = ssm.delta_fwd(*x, h0=dev["h0"], cu_seqlens=cud)
+    h = dev["h0"].clone()
+    y2, hf2 = ssm.delta_fwd(*x, h0=h, h_final=h, cu_seqlens=cud)
+    assert hf2 is h and torch.equal(y, y2) and torch.equal(hf, h) and torch.equal(h[1], dev["h0"][1])
+    rows = dev["v"].flatten(2)[0]
+    for t in (rows, torch.cat([rows] * 30, 1)):
+        want, got = ssm.group_norm_fwd(t, 1, z=t, subtract_mean=True), t.clone()
+        ssm.group_norm_fwd(got, 1, z=t, subtract_mean=True, y=got)
+        assert torch.equal(want, got)
+
+
 @pytest.mark.parametrize("off,width", [(0, 3), (1, 0), (4, 4)])
 def test_rows_off_their_alignment(off, width):
     # bf16 shapes of the tensor cores in rows that do not start on 16 bytes
