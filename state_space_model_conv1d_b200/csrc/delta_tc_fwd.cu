@@ -16,8 +16,9 @@
 // Rounding.  q, k, v are exact bf16.  On the way to the state every factor that
 // is not (h, R, T, u) goes as two bf16 parts with fp32 accumulation (relative
 // 2^-17 each), so h_final is good to about 1e-5 after any number of blocks.
-// What only reaches y (attention weights, u and h of the read-out) is rounded
-// to bf16 once, like y itself.
+// Of what only reaches y the attention weights are rounded to bf16 once, like y
+// itself; u goes as two parts there too (with its high part alone y was off by
+// 2.6e-3 of its norm instead of 2.1e-3, in 1.5 % less time).
 //
 // Roles: 8 warps for the chain (two per lane quarter, half of the columns
 // each), 4 for the output (one thread of them issues its product), one thread
@@ -30,10 +31,10 @@
 // the other and make one operand of 128 rows, and so do the two T of a CTA
 // whose halves are different heads.
 //
-// 4 x 4096 tokens, 32 heads of P 128, N 128: 237 us, 64 blocks one after the
-// other in 128 CTAs, 3.7 us (6.7k cycles) a block: the chain's latency, 36 MMAs
+// 4 x 4096 tokens, 32 heads of P 128, N 128: 240 us, 64 blocks one after the
+// other in 128 CTAs, 3.7 us (6.8k cycles) a block: the chain's latency, 36 MMAs
 // of about 100 cycles and the passes between them.  28301 packed tokens, 64 heads
-// of P 64, two of them in a CTA: 437 us, 7.1k cycles a block.  (With the output's
+// of P 64, two of them in a CTA: 450 us, 7.3k cycles a block.  (With the output's
 // product in the MMA warp, whose waits then queue up behind the products already
 // issued, it was 257 and 472 us.)  The token-by-token form takes 15 times as long
 // on the first call.
@@ -56,7 +57,7 @@ static_assert(kOut0 % 4 == 0, "lane quarters");
 // tensor-memory columns
 constexpr uint32_t TM_H = 0;       // fp32 state, decayed for the next block
 constexpr uint32_t TM_HOP = 128;   // its two bf16 parts: per half of the pass 32 high, 32 low columns
-constexpr uint32_t TM_RU = 256;    // h k, then U (two heads: in 128 columns), then u as an operand (high part)
+constexpr uint32_t TM_RU = 256;    // h k, then U (two heads: in 128 columns), then u (per half 16 columns high, 16 low)
 constexpr uint32_t TM_HQ = 320;    // h q
 constexpr uint32_t TM_O = 384;     // scale exp(cs) h q, to which attention x u is added
 constexpr uint32_t TM_OP = 448;    // R, then the decayed u: two parts of 32 columns
@@ -293,17 +294,13 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
                     arrive_st(B_U0 + b);
                 }
             }
-            // u for the output, over the 32 columns of U that this warp has read
+            // u for the output in two parts, over the 32 columns of U that this warp has read
             if constexpr (ST) {
                 keep(c, p.rec.u(), t0, x, 4);
             } else {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    uint32_t h[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) h[i] = pack2(x[16 * b + 2 * i], x[16 * b + 2 * i + 1]);
-                    tmem_st8(tl + TM_RU + t0 + 8 * b, h);
-                }
+                for (int b = 0; b < 2; ++b)
+                    st_split16(tl + TM_RU + t0 + 8 * b, tl + TM_RU + t0 + 16 + 8 * b, x + 16 * b);
                 arrive_st(B_UOP);
             }
             if (lane == 0) arrive(&ax.mb[B_EMPTY0 + stg]);
@@ -398,8 +395,9 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
 #pragma unroll
                     for (int hh = 0; hh < (DUAL ? 2 : 1); ++hh)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            const uint32_t A = tm + TM_RU + (kk >> 1) * 32 + (kk & 1) * 8;
+                        for (int kp = 0; kp < 8; ++kp) {
+                            const int kk = kp & 3;
+                            const uint32_t A = tm + TM_RU + (kk >> 1) * 32 + (kk & 1) * 8 + (kp >> 2) * 16;
                             const uint64_t B = dP + hh * (kTile >> 4) + kk * 2;
                             if constexpr (DUAL)
                                 mma_ts_lanes(tm + TM_O, A, B, ID5, 1, hh ? ~0u : 0u, hh ? 0u : ~0u);
