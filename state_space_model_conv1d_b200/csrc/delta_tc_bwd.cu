@@ -824,12 +824,21 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
                 x[e] = e <= last ? f * ex2(ci - cj[e]) * x[e] : 0.f;
             }
             if (upper && (unsigned)(i - j0) < 32u) ax.ru[i] = own_x;
+            // from here on x is the rounded value that the matrix holds: in dg the pairs of two tokens behind t come
+            // from dk . k (twice) and from zw, and cancel only if all three are the same number
             uint8_t *row = sm + L::A + 2 * kTile;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                *reinterpret_cast<uint4 *>(row + swz(r, j0 + 8 * k)) =
-                    make_uint4(pack2(x[8 * k], x[8 * k + 1]), pack2(x[8 * k + 2], x[8 * k + 3]),
-                               pack2(x[8 * k + 4], x[8 * k + 5]), pack2(x[8 * k + 6], x[8 * k + 7]));
+            for (int k = 0; k < 4; ++k) {
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float *v = x + 8 * k + 2 * e;
+                    o[e] = pack2(v[0], v[1]);
+                    v[0] = __uint_as_float(o[e] << 16);
+                    v[1] = __uint_as_float(o[e] & 0xffff0000u);
+                }
+                *reinterpret_cast<uint4 *>(row + swz(r, j0 + 8 * k)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
             if (upper) {
                 float kk[32];
                 tc::tmem_ld32(tl + TG_K + j0, kk);

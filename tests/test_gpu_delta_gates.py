@@ -1,0 +1,71 @@
+"""Strong decays and resets of the gated delta rule: the gradient of each gate on the scale of its own token.
+
+dg_t = <d, a_t h_{t-1}> (d the gradient that reaches a_t h_{t-1}), so a token that forgets has a gradient as small
+as its a_t.  Bounds, per token and head:
+
+- token by token in fp32: 2e-5 |d| |a_t h_{t-1}| (the bound of test_gpu_delta.py for gradients);
+- in blocks: every term that does not cancel holds a_t and at most five factors rounded to bf16, 6 * 2^-8
+  |d| |a_t h_{t-1}|, the result's own rounding among them; the others cancel between dq . q and dk . k of the tokens
+  from t to the block's end up to fp32 sums: 16 random roundings of 2^-24 (products of 128 terms, their dot product
+  with q or k of 128 more) of terms that are at most four times their sum, 2 |dq| + 3 |dk| a token (unit q and k),
+  over the block's 64 tokens.
+"""
+import numpy as np
+import pytest
+import torch
+
+import state_space_model_conv1d_b200 as ssm
+
+from layer_ref import HALF, delta_bwd_ref, delta_ref
+from test_gpu_delta import make
+
+pytestmark = pytest.mark.gpu
+GATES = ("q", "k", "v", "g", "beta")
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def gate_norms(r, dy, dh, h0, scale):
+    """|d| |a_t h_{t-1}| of every token and head of one row whose heads share no keys."""
+    _, _, ((_, _, _, path),) = delta_ref(*[r[n] for n in GATES], scale, h0)
+    d, out = dh[0].copy(), np.zeros(r["g"].shape[1:])
+    for t in reversed(range(len(path))):
+        w = path[t][0]
+        kt = r["k"][0, t]
+        d = d + scale * dy[0, t][..., None] * r["q"][0, t][:, None]
+        ds = -r["beta"][0, t][:, None] * np.einsum("hpn,hn->hp", d, kt)
+        d = d + ds[..., None] * kt[:, None]
+        out[t] = np.sqrt((d * d).sum((1, 2)) * (w * w).sum((1, 2)))
+        d = np.exp(r["g"][0, t])[:, None, None] * d
+    return out
+
+
+def forgetful(seed, dtype, T, P, N):
+    """Keys alike, hardly any decay, but for a few tokens of each head that forget."""
+    H = 2
+    dev, _ = make(seed, dtype, 1, T, H, P, H, N, decay=0.01)
+    k = dev["k"].float() + 1.5 * dev["k"][:, :1].float()
+    dev["k"].copy_(k / k.norm(dim=-1, keepdim=True))
+    dev["beta"].mul_(0.5).add_(0.5)
+    for t, h, g in ((7, 0, -12.0), (20, 0, -20.0), (75, 0, -30.0), (5, 1, -20.0), (70, 1, -15.0), (100, 1, -25.0)):
+        dev["g"][0, t, h] = g
+    return dev, {n: f64(dev[n]) for n in (*GATES, "dy", "dh", "h0")}
+
+
+@pytest.mark.parametrize("dtype,P,N", [("f32", 24, 40), ("bf16", 64, 128), ("bf16", 128, 128), ("bf16", 64, 64)])
+def test_gate_gradients_of_tokens_that_forget(dtype, P, N):
+    T = 150
+    dev, r = forgetful(40, dtype, T, P, N)
+    got = ssm.delta_bwd(*[dev[n] for n in GATES], dev["dy"], h0=dev["h0"], dh_final=dev["dh"])
+    want = delta_bwd_ref(*[r[n] for n in GATES], N ** -0.5, r["dy"], r["dh"], r["h0"])
+    own = gate_norms(r, r["dy"], r["dh"], r["h0"], N ** -0.5)
+    tol = (2e-5 if dtype == "f32" else 6 * HALF["bf16"]) * own
+    if dtype == "bf16":
+        s2 = (2 * np.linalg.norm(want["dq"][0], axis=-1) + 3 * np.linalg.norm(want["dk"][0], axis=-1)) ** 2
+        block = np.concatenate([np.tile(s2[i:i + 64].sum(0), (min(64, T - i), 1)) for i in range(0, T, 64)])
+        tol = tol + 16 * 4 * 2.0 ** -24 * np.sqrt(block)
+    err = abs(f64(got["dg"])[0] - want["dg"][0])
+    worst = (err / tol).max()
+    assert worst <= 1, worst
