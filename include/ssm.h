@@ -428,11 +428,11 @@ SSM_API ssm_status ssm_split_fixup(const ssm_scan_args *args, const float *cum_d
  * come in groups shared by nheads / ngroups consecutive heads, as B and C do
  * in ssm_scan_fwd.  The rule is meant for keys of at most unit length and
  * beta in [0, 1]; other values are computed as the formula stands.  g <= 0 is
- * the log decay; g below -100 (-infinity included) counts as -100, whose
- * exp() is zero in fp32.  A NaN or infinity reaches the other tokens of its
- * own 64-token block and everything after it (before it, in the gradients),
- * never another sequence.  Outputs may not overlap inputs or each other,
- * except that h_final may be h0.
+ * the log decay; at or below -104 (-infinity included) a_t is exactly zero, and
+ * so is dg_t: a reset (which does not mend a state that is not finite).  A NaN
+ * or infinity reaches the other tokens of its own 64-token block and everything
+ * after it (before it, in the gradients), never another sequence.  Outputs may
+ * not overlap inputs or each other, except that h_final may be h0.
  *
  * q, k, v, y share one dtype; g and beta are fp32 whatever the dtype, since a
  * log decay summed over a sequence does not survive 8 bits.  bf16 with

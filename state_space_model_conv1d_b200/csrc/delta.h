@@ -5,10 +5,15 @@
 
 namespace ssm {
 
-// exp() of a log decay at or below this is zero in fp32; clamping there keeps
-// a full reset (g = -infinity) out of the prefix sums, where it would give NaN.
-constexpr float kMinLogDecay = -100.f;
+// Log decays at or below this are a reset: exp() rounds to zero in fp32 from
+// -103.98 down.  Clamping there keeps g = -infinity out of the prefix sums,
+// where it would give NaN; decay_of() is then exactly zero, not whatever
+// expf() makes of the bottom of the subnormal range.
+constexpr float kMinLogDecay = -104.f;
 __device__ __forceinline__ float log_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }   // (a NaN stays one)
+
+__device__ __forceinline__ bool resets(float g) { return g <= kMinLogDecay; }
+__device__ __forceinline__ float decay_of(float g) { return resets(g) ? 0.f : expf(g); }
 
 // Token-by-token path (any dtype and sizes).  `ckpt` (may be null) receives
 // the state before every kDeltaCkpt-th token of each sequence.

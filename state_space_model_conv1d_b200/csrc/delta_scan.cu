@@ -94,7 +94,6 @@ template <typename T, int PAD, int kTok, int kThreads> struct Staged {
         for (int i = 0; i < kPer; ++i) dst[threadIdx.x + i * kThreads] = v[i];
     }
 };
-SSM_DEVINL float decay_of(float g) { return expf(log_decay(g)); }
 
 template <int NE, int L>
 SSM_DEVINL void load_row(float (&h)[NE], const float *src, int lrow, int64_t N) {

@@ -727,12 +727,16 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
 
     for (int hh = 0; hh < p.R; ++hh) {
         const int head = grp * p.R + hh;
+        float keep[2];                                 // warp 0: 0 at a reset, whose dg = a <d, h> is exactly zero
         if (warp == 0) {
             const float *gp = a.g + blk.row * a.g_batch_stride + blk.t0 * a.g_token_stride + head;
             const float *bp = a.beta + blk.row * a.beta_batch_stride + blk.t0 * a.beta_token_stride + head;
             double cs[2], last;
-            block_cs(lane < nt ? log_decay(gp[lane * a.g_token_stride]) : 0.f,
-                     lane + 32 < nt ? log_decay(gp[(lane + 32) * a.g_token_stride]) : 0.f, cs[0], cs[1], last);
+            const float g0 = lane < nt ? log_decay(gp[lane * a.g_token_stride]) : 0.f;
+            const float g1 = lane + 32 < nt ? log_decay(gp[(lane + 32) * a.g_token_stride]) : 0.f;
+            keep[0] = resets(g0) ? 0.f : 1.f;
+            keep[1] = resets(g1) ? 0.f : 1.f;
+            block_cs(g0, g1, cs[0], cs[1], last);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int t = lane + 32 * e;
@@ -935,7 +939,7 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
                 const int t = lane + 32 * h;
                 if (t < nt) {
                     const int64_t at = (blk.row * a.seqlen + blk.t0 + t) * H + head;
-                    static_cast<__nv_bfloat16 *>(p.b.dg)[at] = __float2bfloat16_rn(d[h] + last);
+                    static_cast<__nv_bfloat16 *>(p.b.dg)[at] = __float2bfloat16_rn(keep[h] * (d[h] + last));
                     static_cast<__nv_bfloat16 *>(p.b.dbeta)[at] = __float2bfloat16_rn(ax.ru[t] / ax.tab.beta[t]);
                 }
             }

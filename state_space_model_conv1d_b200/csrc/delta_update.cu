@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) delta_update_kernel(const ssm_delta_
     kq += __shfl_xor_sync(~0u, kq, 1);
     kq += __shfl_xor_sync(~0u, kq, 2);
     kq += __shfl_xor_sync(~0u, kq, 4);
-    const float al = expf(log_decay(a.g[b * a.g_batch_stride + h]));
+    const float al = decay_of(a.g[b * a.g_batch_stride + h]);
     const float be = a.beta[b * a.beta_batch_stride + h];
     float *st = a.state + ((slot * H + h) * P) * N;
     if (!SSM_BOUNDS((slot * H + h) * P + p1 - 1, a.nslots * H * P, BS_DELTA_STATE)) return;

@@ -69,3 +69,24 @@ def test_gate_gradients_of_tokens_that_forget(dtype, P, N):
     err = abs(f64(got["dg"])[0] - want["dg"][0])
     worst = (err / tol).max()
     assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("g", [-torch.inf, -104.0])
+@pytest.mark.parametrize("dtype,P,N", [("f32", 24, 40), ("bf16", 24, 40), ("bf16", 64, 128), ("bf16", 128, 64)])
+def test_a_reset_is_exact(dtype, P, N, g):
+    # whatever the state holds, the tokens from the reset on do not know: bit for bit, and no gradient passes
+    dev, _ = make(41, dtype, 1, 150, 2, P, 1, N)
+    x, big = [dev[n] for n in GATES], 1e30 * dev["h0"]
+    for t in (0, 70, 149):
+        x[3].copy_(dev["g"])
+        x[3][:, t] = g
+        y, hf = ssm.delta_fwd(*x)
+        y2, hf2 = ssm.delta_fwd(*x, h0=big)
+        assert torch.equal(y[:, t:], y2[:, t:]) and torch.equal(hf, hf2), t
+        d = ssm.delta_bwd(*x, dev["dy"], h0=dev["h0"], dh_final=dev["dh"])
+        assert (d["dg"][:, t] == 0).all(), t
+        if t == 0:
+            assert (d["dh0"] == 0).all()
+    tok = [v[:, 149] for v in x]
+    zero = torch.zeros_like(big)
+    assert torch.equal(ssm.delta_update(big, *tok), ssm.delta_update(zero, *tok)) and torch.equal(big, zero)
