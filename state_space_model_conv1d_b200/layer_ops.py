@@ -21,7 +21,9 @@ from . import _abi
 from .ops import _dtype_code
 
 _f32, _i32 = torch.float32, torch.int32
-_cur_device, _cur_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# torch's own quick forms of current_device and current_stream, where this torch has them (a CPU-only one does not)
+_cur_device = getattr(torch._C, "_cuda_getDevice", None)
+_cur_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _packer(struct_type):
@@ -52,7 +54,7 @@ def _run(t, stream, body, *args):
     idx = t.get_device()
     if idx < 0:
         raise ValueError("expected a CUDA tensor")
-    if stream is None and idx == _cur_device():
+    if stream is None and _cur_device and _cur_stream and idx == _cur_device():
         return body(*args, _cur_stream(idx))
     with torch.cuda.device(idx):
         s = torch.cuda.current_stream() if stream is None else stream

@@ -14,7 +14,7 @@ import torch
 
 import oracle
 import state_space_model_conv1d_b200 as ssm
-from state_space_model_conv1d_b200 import _abi
+from state_space_model_conv1d_b200 import _abi, layer_ops
 
 from gpu_util import TOL, rel_err
 from layer_ref import HALF, compact_ref, delta_bwd_ref, delta_ref, norm_bwd_ref, norm_ref
@@ -291,6 +291,22 @@ def test_state_pool_past_32_bits():
     refs[idx.long()] = 1
     ssm.state_pages_compact([state], refs, idx)
     assert sorted(idx.tolist()) == [0, 1, 2] and torch.equal(state[idx.long()], kept)
+
+
+def test_without_torchs_private_cuda_names(monkeypatch):
+    # the same call by way of torch's public ones
+    dev, _ = make(16, "f32", 1, 20, 2, 16, 1, 24)
+    x = [dev[n] for n in ("q", "k", "v", "g", "beta")]
+    want = ssm.delta_fwd(*x, h0=dev["h0"])
+    monkeypatch.setattr(layer_ops, "_cur_device", None)
+    monkeypatch.setattr(layer_ops, "_cur_stream", None)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = ssm.delta_fwd(*x, h0=dev["h0"])
+    with torch.cuda.stream(side):
+        there = ssm.delta_fwd(*x, h0=dev["h0"])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(want, got, there))
 
 
 # ------------------------------------------------------ the bounds-checked build

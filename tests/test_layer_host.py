@@ -3,6 +3,7 @@ and every refusal that needs no GPU (nothing here is launched)."""
 import ctypes as C
 import os
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -31,6 +32,17 @@ def test_struct_layouts_match_header(tmp_path):
         assert got[c, "sizeof"] == C.sizeof(py), c
         for f, _ in py._fields_:
             assert got[c, f] == getattr(py, f).offset, (c, f)
+
+
+def test_import_without_torchs_private_cuda_names():
+    # a torch without CUDA lacks them; importing the package looks nothing up
+    code = ("import torch\n"
+            "for n in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "import state_space_model_conv1d_b200 as ssm\n"
+            "assert callable(ssm.delta_fwd) and callable(ssm.scan_fwd)\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
 
 
 def _fill(a, values, at=0):
