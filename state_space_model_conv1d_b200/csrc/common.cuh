@@ -84,6 +84,7 @@ enum BoundsSite {
     BS_CONV_TOKEN, BS_CONV_CHANNEL, BS_CONV_STATE,
     BS_BWD_SEQ, BS_BWD_CHANNEL, BS_SPLIT_ROW, BS_SPLIT_CHANNEL, BS_SSD_SEGMENT,
     BS_DELTA_SEQ, BS_DELTA_STATE, BS_PAGE,
+    BS_DELTA_HEAD, BS_DELTA_SLOT, BS_DELTA_CKPT, BS_DELTA_SHARE, BS_DELTA_OUT, BS_NORM_ROW, BS_NORM_CHANNEL, BS_NORM_SHARE,
 };
 #ifdef SSM_CHECK_BOUNDS
 struct BoundsRecord {

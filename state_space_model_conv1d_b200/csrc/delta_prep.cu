@@ -228,6 +228,9 @@ __global__ void __launch_bounds__(128, 4) delta_prep_kernel(const PrepArgs p, co
     const Block b = find_block(p.cu, p.nseqs, p.seqlen, p.nblk, blockIdx.x);
     if (b.nt == 0) return;
     const int h0 = blockIdx.y * p.heads_per_cta, R = p.H / p.G, grp = h0 / R;
+    if (!SSM_BOUNDS(b.s, p.nseqs, BS_DELTA_SEQ) || !SSM_BOUNDS(b.t0 + b.nt - 1, p.seqlen, BS_DELTA_SEQ) ||
+        !SSM_BOUNDS(seq_slot(p.cu, b.s, p.nblk) + (b.t0 - (p.cu ? p.cu[b.s] : 0)) / kQ - blockIdx.x, 1, BS_DELTA_SLOT) ||
+        !SSM_BOUNDS(h0 + p.heads_per_cta - 1, p.H, BS_DELTA_HEAD)) return;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     if (w == 0) tc::tmem_alloc(&sm.tmem, 64);
     if (tid == 0) {

@@ -36,6 +36,7 @@ struct Args {
     ssm_delta_args a;
     SeqView sv;
     float *ckpt;
+    int64_t ckpt_rows;
 };
 
 // Tokens [lo, hi) of the sequence this CTA owns; row = batch row.
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(W * 32) delta_scan_kernel(const Args p) {
     const int h = blockIdx.x % H, p0 = (int)(blockIdx.x / H) * kRows;
     const int grp = (int)(h / (H / a.ngroups));
     if (!SSM_BOUNDS(sq.hi, a.seqlen + 1, BS_DELTA_SEQ) || !SSM_BOUNDS(sq.lo, sq.hi + 1, BS_DELTA_SEQ)) return;
+    if (p.ckpt && !SSM_BOUNDS(sq.ckpt_row + (sq.hi - sq.lo + kTok - 1) / kTok, p.ckpt_rows + 1, BS_DELTA_CKPT)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lrow = lane % L;
     const int r = warp * Cut<L, W>::per_warp + lane / L;       // row within the CTA
     const bool live = p0 + r < P;
@@ -254,6 +256,7 @@ struct BwdArgs {
     const float *ckpt;
     float *pq, *pk;        // [slices][tokens][H][N]
     float *pg, *pb;        // [slices][tokens][H]
+    int64_t ckpt_rows, slices;
 };
 
 // Sum over the rows of a warp.  With 4 rows lane group i (lanes 8 i .. 8 i + 7)
@@ -303,6 +306,8 @@ __global__ void __launch_bounds__(W * 32, 1) delta_scan_bwd_kernel(const BwdArgs
     const int h = blockIdx.x % H, slice = (int)(blockIdx.x / H), p0 = slice * kRows;
     const int grp = (int)(h / (H / a.ngroups));
     if (!SSM_BOUNDS(sq.hi, a.seqlen + 1, BS_DELTA_SEQ) || !SSM_BOUNDS(sq.lo, sq.hi + 1, BS_DELTA_SEQ)) return;
+    if (!SSM_BOUNDS(sq.ckpt_row + (sq.hi - sq.lo + kTok - 1) / kTok, p.ckpt_rows + 1, BS_DELTA_CKPT) ||
+        !SSM_BOUNDS(p0, P, BS_DELTA_STATE) || !SSM_BOUNDS(slice, p.slices, BS_DELTA_SHARE)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lrow = lane % L;
     const int r = warp * Cut<L, W>::per_warp + lane / L;
     const bool live = p0 + r < P;
@@ -442,6 +447,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_scan_bwd_kernel(const BwdArgs
                     skv += rk[(ti * kWarps + wv) * NP + n];
                 }
                 const int64_t at = (((int64_t)slice * ntok + tok0 + t0 + t) * H + h) * N + n;
+                if (!SSM_BOUNDS(at, p.slices * ntok * H * N, BS_DELTA_SHARE)) continue;
                 p.pq[at] = sqv;
                 p.pk[at] = skv;
             }
@@ -454,8 +460,10 @@ __global__ void __launch_bounds__(W * 32, 1) delta_scan_bwd_kernel(const BwdArgs
                     sb += rb[ti * kWarps + wv];
                 }
                 const int64_t at = ((int64_t)slice * ntok + tok0 + t0 + run * TR + ti) * H + h;
-                p.pg[at] = sg;
-                p.pb[at] = sb;
+                if (SSM_BOUNDS(at, p.slices * ntok * H, BS_DELTA_SHARE)) {
+                    p.pg[at] = sg;
+                    p.pb[at] = sb;
+                }
             }
             __syncthreads();
         }
@@ -515,6 +523,8 @@ __global__ void __launch_bounds__(W * 32, 1) delta_rows_bwd_kernel(const BwdArgs
     const int h = blockIdx.x % H, slice = (int)(blockIdx.x / H), p0 = slice * kRows;
     const int grp = (int)(h / (H / a.ngroups));
     if (!SSM_BOUNDS(sq.hi, a.seqlen + 1, BS_DELTA_SEQ) || !SSM_BOUNDS(sq.lo, sq.hi + 1, BS_DELTA_SEQ)) return;
+    if (!SSM_BOUNDS(sq.ckpt_row + (sq.hi - sq.lo + kTok - 1) / kTok, p.ckpt_rows + 1, BS_DELTA_CKPT) ||
+        !SSM_BOUNDS(p0, P, BS_DELTA_STATE) || !SSM_BOUNDS(slice, p.slices, BS_DELTA_SHARE)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lrow = lane % L;
     const int r = warp * Cut<L, W>::per_warp + lane / L, n0 = lrow * 4;    // this lane's row and first state
     const bool live = p0 + r < P;
@@ -658,6 +668,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_rows_bwd_kernel(const BwdArgs
                     skv += bk[(ti * W + wv) * NP + n];
                 }
                 const int64_t at = (((int64_t)slice * ntok + tok0 + t0 + first + ti) * H + h) * N + n;
+                if (!SSM_BOUNDS(at, p.slices * ntok * H * N, BS_DELTA_SHARE)) continue;
                 p.pq[at] = sqv;
                 p.pk[at] = skv;
             }
@@ -672,8 +683,10 @@ __global__ void __launch_bounds__(W * 32, 1) delta_rows_bwd_kernel(const BwdArgs
                 }
                 if (lane == 0) {
                     const int64_t at = ((int64_t)slice * ntok + tok0 + t0 + first + ti) * H + h;
-                    p.pg[at] = sg;
-                    p.pb[at] = sb;
+                    if (SSM_BOUNDS(at, p.slices * ntok * H, BS_DELTA_SHARE)) {
+                        p.pg[at] = sg;
+                        p.pb[at] = sb;
+                    }
                 }
             }
         }
@@ -801,7 +814,7 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 cudaError_t launch_delta_simt(const ssm_delta_args &a, const SeqView &sv, float *ckpt, cudaStream_t st) {
     if (seqs_of(a) == 0) return cudaSuccess;
-    const Args p{a, sv, ckpt};
+    const Args p{a, sv, ckpt, delta_ckpt_rows(a)};
     return a.dtype == SSM_BF16 ? pick_fwd<__nv_bfloat16>(p, st) : pick_fwd<float>(p, st);
 }
 
@@ -819,7 +832,7 @@ cudaError_t launch_delta_simt_bwd(const ssm_delta_bwd_args &b, const SeqView &sv
     float *ckpt = reinterpret_cast<float *>(at);
     at += up256((size_t)delta_ckpt_rows(a) * a.nheads * a.headdim * a.dstate * 4);
     const size_t tok = (size_t)(a.batch * a.seqlen) * a.nheads * slices_of(a) * 4;
-    BwdArgs p{b, sv, ckpt, nullptr, nullptr, nullptr, nullptr};
+    BwdArgs p{b, sv, ckpt, nullptr, nullptr, nullptr, nullptr, delta_ckpt_rows(a), slices_of(a)};
     p.pq = reinterpret_cast<float *>(at); at += up256(tok * a.dstate);
     p.pk = reinterpret_cast<float *>(at); at += up256(tok * a.dstate);
     p.pg = reinterpret_cast<float *>(at); at += up256(tok);

@@ -88,7 +88,7 @@ struct Args {
     SeqView sv;
     const uint8_t *prep;
     Rec rec;
-    int64_t nblk;
+    int64_t nblk, slots;
     int R, nsl, units;
 };
 
@@ -138,6 +138,8 @@ delta_bwd_chain_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, c
         return;
     }
     const int64_t slot0 = seq_slot(a.cu_seqlens, s, p.nblk);
+    if (!SSM_BOUNDS(slot0 + n - 1, p.slots, BS_DELTA_SLOT) || !SSM_BOUNDS(max(head[0], head[1]), H, BS_DELTA_HEAD) ||
+        !SSM_BOUNDS(max(row0[0], row0[1]), P, BS_DELTA_STATE)) return;
     if (warp == 0) tc::tmem_alloc(&ax.tmem, kTmemCols);
     if (tid == 0) {
         constexpr int kEmpty = 1 + kChainWarps + kSideWarps;
@@ -415,7 +417,7 @@ delta_bwd_chain_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, c
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int t = 2 * q + (lane >> 4) + 8 * i;
-                    if (t < nt)
+                    if (t < nt && SSM_BOUNDS(lo + (int64_t)(n - 1 - it) * kQ + t, a.seqlen, BS_DELTA_OUT))
                         *reinterpret_cast<uint4 *>(o + (int64_t)t * H * P) = *reinterpret_cast<const uint4 *>(vs + t * 128 + ch * 8);
                 }
             }
@@ -662,6 +664,8 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
     const bool upper = r >= 64;                                                          // a dk row
     const int64_t H = a.nheads, N = a.dstate;
     const int nt = blk.nt;
+    if (!SSM_BOUNDS(blk.s, p.sv.nseqs, BS_DELTA_SEQ) || !SSM_BOUNDS(blk.t0 + nt - 1, a.seqlen, BS_DELTA_OUT) ||
+        !SSM_BOUNDS(grp * p.R + p.R - 1, H, BS_DELTA_HEAD)) return;
     if (warp == 0) tc::tmem_alloc(&ax.tmem, 512);
     if (tid == 0) {
         tc::mbar_init(&ax.full, 1);
@@ -1025,6 +1029,7 @@ cudaError_t launch_delta_tc_bwd(const ssm_delta_bwd_args &b, const SeqView &sv, 
     p.sv = sv;
     p.prep = prep;
     p.nblk = delta_blocks_per_row(a);
+    p.slots = delta_slots(a);
     p.R = (int)(a.nheads / a.ngroups);
     p.nsl = (int)((a.headdim + 63) / 64);
     p.units = (p.R * p.nsl + 1) / 2;

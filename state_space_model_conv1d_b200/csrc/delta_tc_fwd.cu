@@ -99,7 +99,7 @@ struct Args {
     ssm_delta_args a;
     SeqView sv;
     const uint8_t *prep;           // delta_prep.cu: [slot][H][kHeadBytes]
-    int64_t nblk;
+    int64_t nblk, slots;
     int R, nsl, units;             // heads per group, 64-row slices per head, CTAs per group
     Rec rec;                       // the states' pass of the backward: where u and the states go
 };
@@ -154,6 +154,8 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
         return;
     }
     const int64_t slot0 = seq_slot(a.cu_seqlens, s, p.nblk);
+    if (!SSM_BOUNDS(slot0 + n - 1, p.slots, BS_DELTA_SLOT) || !SSM_BOUNDS(max(head[0], head[1]), H, BS_DELTA_HEAD) ||
+        !SSM_BOUNDS(max(row0[0], row0[1]), P, BS_DELTA_STATE)) return;
     if (warp == 0) tc::tmem_alloc(&ax.tmem, kTmemCols);
     if (tid == 0) {
         constexpr int kEmpty = 1 + kChainWarps + (ST ? 0 : 1 + kOutWarps);
@@ -424,7 +426,7 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int t = 2 * q + (lane >> 4) + 8 * i;
-                    if (t < nt)
+                    if (t < nt && SSM_BOUNDS(lo + (int64_t)c * kQ + t, a.seqlen, BS_DELTA_OUT))
                         *reinterpret_cast<uint4 *>(yc + t * a.y_token_stride) =
                             *reinterpret_cast<const uint4 *>(ys + t * 128 + ch * 8);
                 }
@@ -629,6 +631,7 @@ cudaError_t launch_delta_chain(const ssm_delta_args &a, const SeqView &sv, const
     p.sv = sv;
     p.prep = static_cast<const uint8_t *>(prep);
     p.nblk = delta_blocks_per_row(a);
+    p.slots = delta_slots(a);
     p.R = (int)(a.nheads / a.ngroups);
     p.nsl = (int)((a.headdim + 63) / 64);
     p.units = (p.R * p.nsl + 1) / 2;

@@ -30,6 +30,7 @@ struct Args {
     float *pw, *pb;          // [splits][channels] shares of dweight, dbias
     int64_t rows;            // batch * seqlen
     int splits;              // units per group
+    int64_t share;           // values that each share array has room for
 };
 
 // Sum of u (and of v) over the unit's TPU threads; every thread gets it.
@@ -138,6 +139,12 @@ SSM_DEVINL void split_row(const ssm_norm_args &a, int64_t row, int64_t &b, int64
     }
 }
 
+// Whether the row and its channels up to c lie in the tensors (the bounds-checked build; else true).
+SSM_DEVINL bool in_tensor(const ssm_norm_args &a, int64_t b, int64_t t, int64_t c) {
+    return SSM_BOUNDS(b, a.batch, BS_NORM_ROW) && SSM_BOUNDS(t, a.seqlen, BS_NORM_ROW) &&
+           SSM_BOUNDS(c, a.channels, BS_NORM_CHANNEL);
+}
+
 template <int TPU> constexpr int threads_of() { return TPU > 256 ? TPU : 256; }
 // What z does: nothing, gate the result, gate the input.
 enum Kind { kNoGate, kGate, kGateFirst };
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(threads_of<TPU>()) group_norm_kernel(const Arg
         const bool live = first < p.splits && row < p.rows;
         int64_t bi, t;
         split_row(a, live ? row : 0, bi, t);
-        const int dl = live ? D : 0;
+        const int dl = live && in_tensor(a, bi, t, c0 + D - 1) ? D : 0;
         load<T, TPU, VPT, VEC>(x, (const T *)a.x + bi * a.x_batch_stride + t * a.x_token_stride + c0, th, dl);
         if (K != kNoGate)
             load<T, TPU, VPT, VEC>(z, (const T *)a.z + bi * a.z_batch_stride + t * a.z_token_stride + c0, th, dl);
@@ -220,6 +227,7 @@ __global__ void __launch_bounds__(threads_of<TPU>()) group_norm_kernel(const Arg
         if (live) {
             int64_t bi, t;
             split_row(a, row, bi, t);
+            const int ds = in_tensor(a, bi, t, c0 + D - 1) ? D : 0;
             T *y = (T *)a.y + bi * a.y_batch_stride + t * a.y_token_stride + c0;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
@@ -231,7 +239,7 @@ __global__ void __launch_bounds__(threads_of<TPU>()) group_norm_kernel(const Arg
                     if (K == kNoGate && act) v *= sigmoid(v);
                     o[e] = v;
                 }
-                store<T, TPU, VPT, VEC>(y, o, th, i, D);
+                store<T, TPU, VPT, VEC>(y, o, th, i, ds);
             }
         }
         x = xn;
@@ -269,7 +277,7 @@ __global__ void __launch_bounds__(threads_of<TPU>(), VPT == 1 ? 2 : 1) group_nor
         const bool live = first < p.splits && row < p.rows;
         int64_t bi, t;
         split_row(a, live ? row : 0, bi, t);
-        const int dl = live ? D : 0;
+        const int dl = live && in_tensor(a, bi, t, c0 + D - 1) ? D : 0;
         load<T, TPU, VPT, VEC>(x, (const T *)a.x + bi * a.x_batch_stride + t * a.x_token_stride + c0, th, dl);
         load<T, TPU, VPT, VEC>(g, (const T *)p.dy + bi * p.dy_bs + t * p.dy_ts + c0, th, dl);
         if (K != kNoGate)
@@ -322,6 +330,7 @@ __global__ void __launch_bounds__(threads_of<TPU>(), VPT == 1 ? 2 : 1) group_nor
         if (live) {
             s1 = a.subtract_mean ? s1 * inv : 0.f;
             s2 *= inv;
+            const int ds = SSM_BOUNDS(row * a.channels + c0 + D - 1, p.rows * a.channels, BS_NORM_ROW) ? D : 0;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 float o[8], o2[8];
@@ -337,8 +346,8 @@ __global__ void __launch_bounds__(threads_of<TPU>(), VPT == 1 ? 2 : 1) group_nor
                         o2[e] = dz[K == kGate ? i : 0][e];
                     }
                 }
-                store<T, TPU, VPT, VEC>((T *)p.dx + row * a.channels + c0, o, th, i, D);
-                if (K != kNoGate) store<T, TPU, VPT, VEC>((T *)p.dz + row * a.channels + c0, o2, th, i, D);
+                store<T, TPU, VPT, VEC>((T *)p.dx + row * a.channels + c0, o, th, i, ds);
+                if (K != kNoGate) store<T, TPU, VPT, VEC>((T *)p.dz + row * a.channels + c0, o2, th, i, ds);
             }
         }
         if (VPT <= 2) {
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(threads_of<TPU>(), VPT == 1 ? 2 : 1) group_nor
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = chan<TPU, VEC>(th, i, e);
-                if (c < D) {
+                if (c < D && SSM_BOUNDS(first * a.channels + c0 + c, p.share, BS_NORM_SHARE)) {
                     p.pw[first * a.channels + c0 + c] = dw[i][e];
                     p.pb[first * a.channels + c0 + c] = db[i][e];
                 }
@@ -512,7 +521,9 @@ cudaError_t launch_group_norm_bwd(const ssm_norm_bwd_args &b, void *ws, cudaStre
     }
     if (b.dweight || b.dbias) {
         p.pw = static_cast<float *>(ws);
-        p.pb = reinterpret_cast<float *>(static_cast<char *>(ws) + group_norm_bwd_workspace_bytes(b) / 2);
+        const size_t half = group_norm_bwd_workspace_bytes(b) / 2;
+        p.pb = reinterpret_cast<float *>(static_cast<char *>(ws) + half);
+        p.share = (int64_t)(half / 4);
     }
     const size_t es = a.dtype == SSM_BF16 ? 2 : 4;
     const bool vec = (a.channels / a.groups) % 8 == 0 && vec_ok(a.x, a.x_batch_stride, a.x_token_stride, es) &&

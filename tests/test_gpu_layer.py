@@ -325,6 +325,35 @@ def test_checked_build_runs_clean(monkeypatch):
     assert rec[0].value == 0, f"bounds check fired: site {rec[1].value}, index {rec[2].value}, extent {rec[3].value}"
 
 
+def test_checked_build_runs_clean_beyond_one_block(monkeypatch):
+    # remainders of every kind: rows, widths, slices and blocks that fill nothing, several heads in a pre-pass CTA,
+    # units of several tokens
+    import test_gpu_delta_paths as paths
+    import test_gpu_norm_turns as turns
+    from test_gpu_norm import check as check_norm
+    chk = _abi.checked_lib()
+    rec = [C.c_int32(-1), C.c_int32(-1), C.c_int64(-1), C.c_int64(-1)]
+    assert chk.ssm_bounds_record(*[C.byref(r) for r in rec], 1) == _abi.SSM_OK
+    monkeypatch.setattr(_abi, "lib", lambda: chk)
+    lengths = [70, 0, 1, 64, 200]
+    for dtype, H, P, G, N in (("bf16", 6, 40, 2, 72), ("bf16", 3, 192, 1, 72), ("bf16", 4, 8, 1, 8), ("f32", 12, 33, 3, 70),
+                              ("bf16", 12, 35, 4, 200), ("f32", 2, 9, 1, 60), ("f32", 2, 20, 1, 200)):
+        check_fwd(dtype, 1, sum(lengths), H, P, G, N, lengths, seed=17)
+        check_bwd(dtype, 1, sum(lengths), H, P, G, N, lengths, seed=18)
+        check_bwd(dtype, 2, 65, H, P, G, N, seed=19)
+    paths.test_heads_of_a_group_share_a_prepass(3, 3, 2700)
+    for dtype, D in (("bf16", 64), ("f32", 63), ("bf16", 511), ("f32", 2048), ("bf16", 7001)):
+        turns.test_units_of_several_tokens(dtype, D)
+    check_norm("bf16", (3, 41), 2 * 333, 2, "first", True, seed=20)
+    dev, _ = make(21, "bf16", 3, 1, 4, 33, 2, 41)
+    pool = torch.randn(5, 4, 33, 41, device="cuda")
+    ssm.delta_update(pool, *[dev[n][:, 0] for n in ("q", "k", "v", "g", "beta")],
+                     state_batch_indices=torch.tensor([4, -1, 0], dtype=torch.int32, device="cuda"))
+    ssm.state_pages_copy([pool], *[torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([4, -1, 9], [1, 2, 3])])
+    assert chk.ssm_bounds_record(*[C.byref(r) for r in rec], 0) == _abi.SSM_OK
+    assert rec[0].value == 0, f"bounds check fired: site {rec[1].value}, index {rec[2].value}, extent {rec[3].value}"
+
+
 # ---------------------------------------------------------------------- refusals
 def test_binding_refuses():
     dev, _ = make(14, "bf16", 2, 9, 4, 8, 2, 16)
