@@ -456,14 +456,16 @@ typedef struct ssm_delta_args {
     float *h_final;           /* [nseq][H][P][N] or NULL */
     const int32_t *cu_seqlens;/* [nseqs+1] device int32, or NULL */
     float scale;
-    int32_t reserved0;
+    int32_t gates_f32;        /* ssm_delta_bwd: 1 = dg and dbeta are fp32, 0 = in dtype */
 } ssm_delta_args;
 
 /* Backward of ssm_delta_fwd: gradients of sum(dy * y) + sum(dh_final *
  * h_final) for the call `fwd` describes (its y and h_final are ignored).
  * Gradients are contiguous.  dq, dk [b][T][G*N] (summed over the heads of a
  * group), dv [b][T][H*P], dg, dbeta [b][T][H] are in the activations' dtype,
- * each rounded once; dh0 [nseq][H][P][N] is fp32 and may be NULL.  Sums run
+ * each rounded once; dg and dbeta in fp32, unrounded, with fwd.gates_f32 (what
+ * a caller wants who adds them over the tokens into the gates' parameters).
+ * dh0 [nseq][H][P][N] is fp32 and may be NULL.  Sums run
  * in a fixed order: the same call gives the same bits. */
 typedef struct ssm_delta_bwd_args {
     ssm_delta_args fwd;

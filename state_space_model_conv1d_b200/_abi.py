@@ -108,7 +108,7 @@ class DeltaArgs(C.Structure):
         ("beta", _vp), ("beta_batch_stride", _i64), ("beta_token_stride", _i64),
         ("y", _vp), ("y_batch_stride", _i64), ("y_token_stride", _i64),
         ("h0", _vp), ("h_final", _vp), ("cu_seqlens", _vp),
-        ("scale", C.c_float), ("reserved0", _i32),
+        ("scale", C.c_float), ("gates_f32", _i32),
     ]
 
 

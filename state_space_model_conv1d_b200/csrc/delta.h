@@ -1,6 +1,7 @@
 // delta.h -- host-side launchers of the gated delta rule (internal to libssm).
 #pragma once
 
+#include "common.cuh"
 #include "launch.h"
 
 namespace ssm {
@@ -14,6 +15,18 @@ __device__ __forceinline__ float log_decay(float g) { return g < kMinLogDecay ? 
 
 __device__ __forceinline__ bool resets(float g) { return g <= kMinLogDecay; }
 __device__ __forceinline__ float decay_of(float g) { return resets(g) ? 0.f : expf(g); }
+
+// dg and dbeta of gate i: fp32 or the activations' type T.
+template <typename T>
+__device__ __forceinline__ void store_gates(const ssm_delta_bwd_args &b, int64_t i, float dg, float dbeta) {
+    if (b.fwd.gates_f32) {
+        static_cast<float *>(b.dg)[i] = dg;
+        static_cast<float *>(b.dbeta)[i] = dbeta;
+    } else {
+        Elem<T>::st(static_cast<T *>(b.dg) + i, dg);
+        Elem<T>::st(static_cast<T *>(b.dbeta) + i, dbeta);
+    }
+}
 
 // Token-by-token path (any dtype and sizes).  `ckpt` (may be null) receives
 // the state before every kDeltaCkpt-th token of each sequence.

@@ -722,8 +722,7 @@ __global__ void delta_shares_kernel(const BwdArgs p, int slices) {
             sg += p.pg[(int64_t)s * ntok * H + i];
             sb += p.pb[(int64_t)s * ntok * H + i];
         }
-        Elem<T>::st((T *)p.b.dg + i, sg);
-        Elem<T>::st((T *)p.b.dbeta + i, sb);
+        store_gates<T>(p.b, i, sg, sb);
     }
 }
 

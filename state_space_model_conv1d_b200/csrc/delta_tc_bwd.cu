@@ -943,8 +943,7 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
                 const int t = lane + 32 * h;
                 if (t < nt) {
                     const int64_t at = (blk.row * a.seqlen + blk.t0 + t) * H + head;
-                    static_cast<__nv_bfloat16 *>(p.b.dg)[at] = __float2bfloat16_rn(keep[h] * (d[h] + last));
-                    static_cast<__nv_bfloat16 *>(p.b.dbeta)[at] = __float2bfloat16_rn(ax.ru[t] / ax.tab.beta[t]);
+                    store_gates<__nv_bfloat16>(p.b, at, keep[h] * (d[h] + last), ax.ru[t] / ax.tab.beta[t]);
                 }
             }
         }

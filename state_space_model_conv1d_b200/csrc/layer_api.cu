@@ -73,10 +73,13 @@ ssm_status validate_delta_bwd(const ssm_delta_bwd_args *b) {
     f.y_batch_stride = b->dy_batch_stride;
     f.y_token_stride = b->dy_token_stride;
     SSM_TRY(validate_delta(&f));
+    if (f.gates_f32 != 0 && f.gates_f32 != 1) return SSM_ERR_INVALID_ARG;
     if (f.batch > 0 && f.seqlen > 0 && (!b->dq || !b->dk || !b->dv || !b->dg || !b->dbeta)) return SSM_ERR_INVALID_ARG;
     const size_t es = esize(f.dtype);
-    for (const void *o : {b->dq, b->dk, b->dv, b->dg, b->dbeta})
+    for (const void *o : {b->dq, b->dk, b->dv})
         if (!aligned(o, es)) return SSM_ERR_ALIGNMENT;
+    for (const void *o : {b->dg, b->dbeta})
+        if (!aligned(o, f.gates_f32 ? 4 : es)) return SSM_ERR_ALIGNMENT;
     if (!aligned(b->dh_final, 4) || !aligned(b->dh0, 4)) return SSM_ERR_ALIGNMENT;
     return SSM_OK;
 }

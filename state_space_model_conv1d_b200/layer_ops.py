@@ -116,7 +116,7 @@ def _check_dims(q, v):
         raise ValueError("q, k are [b, T, G, N] and v is [b, T, H, P]")
 
 
-def _delta_args(q, k, v, g, beta, y, y_name, scale, h0, h_final, cu_seqlens):
+def _delta_args(q, k, v, g, beta, y, y_name, scale, h0, h_final, cu_seqlens, gates_f32=0):
     """The fields of ``ssm_delta_args`` in order, and the number of sequences."""
     idx, dt = v.get_device(), v.dtype
     b, T, H, P = v.shape
@@ -134,7 +134,7 @@ def _delta_args(q, k, v, g, beta, y, y_name, scale, h0, h_final, cu_seqlens):
             _act(beta, "beta", idx, gates, _f32), *_strides(beta, 2, "beta"),
             _act(y, y_name, idx, v.shape, dt), *_strides(y, 2, y_name),
             _dense(h0, "h0", idx, hshape, _f32), _dense(h_final, "h_final", idx, hshape, _f32), cu,
-            N ** -0.5 if scale is None else scale, 0), nseq
+            N ** -0.5 if scale is None else scale, gates_f32), nseq
 
 
 def delta_fwd(q, k, v, g, beta, *, scale=None, h0=None, cu_seqlens=None, y=None, h_final=None,
@@ -164,28 +164,33 @@ def _delta_fwd(q, k, v, g, beta, scale, h0, cu_seqlens, y, h_final, return_final
 
 
 def delta_bwd(q, k, v, g, beta, dy, *, scale=None, h0=None, cu_seqlens=None, dh_final=None, out=None,
-              workspace=None, stream=None):
+              gate_dtype=None, workspace=None, stream=None):
     """Gradients of ``sum(dy * y) + sum(dh_final * h_final)`` of :func:`delta_fwd`.
 
     Returns a dict of contiguous tensors: ``dq, dk, dv, dg, dbeta`` in v's dtype
-    and ``dh0`` fp32 (always, also for ``h0=None``).  ``out`` (such a dict) is
-    filled instead of allocating.
+    and ``dh0`` fp32 (always, also for ``h0=None``).  ``gate_dtype=torch.float32``
+    gives ``dg`` and ``dbeta`` in fp32, as the gates themselves are: for gradients
+    that are added over the tokens.  ``out`` (such a dict) is filled instead of
+    allocating.
     """
-    return _run(v, stream, _delta_bwd, q, k, v, g, beta, dy, scale, h0, cu_seqlens, dh_final, out, workspace)
+    return _run(v, stream, _delta_bwd, q, k, v, g, beta, dy, scale, h0, cu_seqlens, dh_final, out, gate_dtype, workspace)
 
 
-def _delta_bwd(q, k, v, g, beta, dy, scale, h0, cu_seqlens, dh_final, out, workspace, s):
+def _delta_bwd(q, k, v, g, beta, dy, scale, h0, cu_seqlens, dh_final, out, gate_dtype, workspace, s):
     _check_dims(q, v)
-    fwd, nseq = _delta_args(q, k, v, g, beta, dy, "dy", scale, h0, None, cu_seqlens)
     idx, dt = v.get_device(), v.dtype
+    gdt = dt if gate_dtype is None else gate_dtype
+    if gdt not in (dt, _f32):
+        raise TypeError(f"gate_dtype must be {dt} or torch.float32, got {gdt}")
+    fwd, nseq = _delta_args(q, k, v, g, beta, dy, "dy", scale, h0, None, cu_seqlens, 1 if gdt == _f32 else 0)
     hshape = (nseq, v.shape[2], v.shape[3], q.shape[3])
     if out is None:
-        out = dict(dq=_new(v, q.shape), dk=_new(v, k.shape), dv=_new(v), dg=_new(v, g.shape),
-                   dbeta=_new(v, beta.shape), dh0=_new(v, hshape, _f32))
+        out = dict(dq=_new(v, q.shape), dk=_new(v, k.shape), dv=_new(v), dg=_new(v, g.shape, gdt),
+                   dbeta=_new(v, beta.shape, gdt), dh0=_new(v, hshape, _f32))
     a = _pack_delta_bwd(*fwd, dy.data_ptr(), *_strides(dy, 2, "dy"), _dense(dh_final, "dh_final", idx, hshape, _f32),
                         _dense(out["dq"], "dq", idx, q.shape, dt), _dense(out["dk"], "dk", idx, k.shape, dt),
-                        _dense(out["dv"], "dv", idx, v.shape, dt), _dense(out["dg"], "dg", idx, g.shape, dt),
-                        _dense(out["dbeta"], "dbeta", idx, beta.shape, dt),
+                        _dense(out["dv"], "dv", idx, v.shape, dt), _dense(out["dg"], "dg", idx, g.shape, gdt),
+                        _dense(out["dbeta"], "dbeta", idx, beta.shape, gdt),
                         _dense(out.get("dh0"), "dh0", idx, hshape, _f32))
     l = _abi.lib()
     workspace = _workspace(workspace, l.ssm_delta_bwd_workspace_size(a), v, idx)

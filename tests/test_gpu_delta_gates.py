@@ -90,3 +90,34 @@ def test_a_reset_is_exact(dtype, P, N, g):
     tok = [v[:, 149] for v in x]
     zero = torch.zeros_like(big)
     assert torch.equal(ssm.delta_update(big, *tok), ssm.delta_update(zero, *tok)) and torch.equal(big, zero)
+
+
+@pytest.mark.parametrize("dtype,P,N", [("f32", 24, 40), ("bf16", 24, 41), ("bf16", 64, 128), ("bf16", 128, 64)])
+def test_gate_gradients_in_fp32(dtype, P, N):
+    # the same numbers without their last rounding: rounded once they are the default's, and their sums over the
+    # tokens do not carry 8-bit errors
+    dev, r = make(42, dtype, 2, 200, 4, P, 2, N)
+    call = lambda **kw: ssm.delta_bwd(*[dev[n] for n in GATES], dev["dy"], h0=dev["h0"], dh_final=dev["dh"], **kw)
+    d, f = call(), call(gate_dtype=torch.float32)
+    assert f["dg"].dtype == f["dbeta"].dtype == torch.float32
+    assert all(torch.equal(d[n], f[n].to(d[n].dtype)) for n in d)
+    out = {n: torch.full_like(t, torch.nan) for n, t in f.items()}
+    assert call(gate_dtype=torch.float32, out=out) is out and all(torch.equal(out[n], f[n]) for n in f)
+    want = delta_bwd_ref(*[r[n] for n in GATES], N ** -0.5, r["dy"], r["dh"], r["h0"])
+    if N % 8 or dtype == "f32":              # token by token: fp32 throughout
+        for n in ("dg", "dbeta"):
+            assert abs(f64(f[n]) - want[n]).max() <= 2e-5 * abs(want[n]).max(), n
+
+
+def test_gate_dtype_refusals():
+    dev, _ = make(43, "bf16", 1, 20, 2, 64, 1, 64)
+    x = [dev[n] for n in GATES]
+    with pytest.raises(TypeError):
+        ssm.delta_bwd(*x, dev["dy"], gate_dtype=torch.float16)
+    with pytest.raises(TypeError):
+        ssm.delta_bwd(*[t.float() for t in x], dev["dy"].float(), gate_dtype=torch.bfloat16)
+    out = ssm.delta_bwd(*x, dev["dy"])
+    with pytest.raises(TypeError):
+        ssm.delta_bwd(*x, dev["dy"], gate_dtype=torch.float32, out=out)
+    with pytest.raises(TypeError):
+        ssm.delta_bwd(*x, dev["dy"], out=ssm.delta_bwd(*x, dev["dy"], gate_dtype=torch.float32))

@@ -129,6 +129,19 @@ def test_delta_bwd_rejects(kw, status):
     assert _abi.lib().ssm_delta_bwd(C.byref(_set(b, kw)), None, 0, None) == status
 
 
+@pytest.mark.parametrize("flag,dg,status", [(0, FAKE + 2, WORKSPACE), (1, FAKE + 2, ALIGNMENT), (1, FAKE + 4, WORKSPACE),
+                                            (2, FAKE, INVALID), (-1, FAKE, INVALID)])
+def test_delta_bwd_gates_f32(flag, dg, status):
+    b = _abi.DeltaBwdArgs()
+    b.fwd = _delta(gates_f32=flag)
+    b.dy, b.dy_batch_stride, b.dy_token_stride = FAKE, 25600, 256
+    b.dq = b.dk = b.dv = b.dh0 = FAKE
+    for name in ("dg", "dbeta"):
+        b.dg = b.dbeta = FAKE
+        setattr(b, name, dg)
+        assert _abi.lib().ssm_delta_bwd(C.byref(b), None, 0, None) == status
+
+
 def test_delta_workspace():
     lib = _abi.lib()
     size = lambda **kw: lib.ssm_delta_workspace_size(C.byref(_delta(**kw)))
