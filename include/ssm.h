@@ -429,7 +429,9 @@ SSM_API ssm_status ssm_split_fixup(const ssm_scan_args *args, const float *cum_d
  * in ssm_scan_fwd.  The rule is meant for keys of at most unit length and
  * beta in [0, 1]; other values are computed as the formula stands.  g <= 0 is
  * the log decay; at or below -104 (-infinity included) a_t is exactly zero, and
- * so is dg_t: a reset (which does not mend a state that is not finite).  A NaN
+ * so is dg_t: a reset (which does not mend a state that is not finite).  On the
+ * tensor cores a subnormal a_t, g below -87.3, is zero as well, and growth, g > 0,
+ * is computed as long as exp() of its sum over 64 tokens is finite in fp32.  A NaN
  * or infinity reaches the other tokens of its own 64-token block and everything
  * after it (before it, in the gradients), never another sequence.  Outputs may
  * not overlap inputs or each other, except that h_final may be h0.
@@ -552,7 +554,8 @@ SSM_API ssm_status ssm_group_norm_bwd(const ssm_norm_bwd_args *args, void *works
  * pool (a state pool [nslots][H][P][N] and a conv pool [nslots][conv_dim][K-1],
  * say), the slots that ssm_state_update, ssm_delta_update and the
  * intermediate states of ssm_scan_fwd address.  `refs` [nslots] counts the
- * holders of each page on the device; 0 marks a free one.  All calls run
+ * holders of each page on the device; 0 marks a free one (a fork sets 1; the
+ * caller adds one for each further holder).  All calls run
  * without a host round trip, and equal inputs give equal pages: the lowest
  * free page goes first.
  *

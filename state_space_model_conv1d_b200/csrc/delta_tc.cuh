@@ -225,7 +225,7 @@ SSM_DEVINL void block_cs(float g0, float g1, double &c0, double &c1, double &las
 }
 SSM_DEVINL float exp_d(double x) { return ex2((float)(x * 1.4426950408889634)); }
 
-// The sequence and block of a packed slot (see delta_slot below); c < 0: none.
+// The sequence and block of a slot of per-block data (seq_slot is its inverse; nt = 0: none).
 struct Block {
     int s;          // sequence
     int64_t row;    // batch row

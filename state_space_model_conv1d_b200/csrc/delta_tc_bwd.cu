@@ -12,7 +12,7 @@
 //   dbeta_i = dR_i . u_i / beta_i,
 //   dg_t = sum_{i >= t} (dq_i . q_i - dk_i . k_i + 2 dR_i . (u_i - beta_i v_i)) + <h_out, d>.
 //
-// The last line: every factor exp(cs_i - cs_j) weighs a product of q_i or k_i
+// The line of dg: every factor exp(cs_i - cs_j) weighs a product of q_i or k_i
 // on the side of i and of k_j on that of j, so the sums over a row or a column
 // are dot products of the finished gradients with q and k, and no second pass
 // over the 64 x 64 matrices is needed; u - beta v = -beta (exp(cs) h k + sum e (k.k) u).
@@ -23,9 +23,18 @@
 // that makes dq, dk, dg and dbeta of all the group's heads, so that dq and dk
 // are summed in a fixed order and rounded once.
 //
+// dg_t is a difference: terms of two tokens behind t stand in dq . q, in dk . k
+// and in dR . (u - beta v) and cancel.  All of them use the same rounded matrix,
+// so what is left of them is the rounding of fp32 sums: 5e-6 where the block's
+// terms are about 1, whatever a_t is.  Every other term holds a_t itself.
+//
 // Rounding: on the way to dh0 every factor that is not exact goes as two bf16
-// parts (as in the forward); what ends in a bf16 gradient is rounded to bf16
-// once per factor.
+// parts (as in the forward), and so does all of dv but its own rounding (1.7e-3
+// of its norm).  The last launch takes h, d, dR, u and the matrices A and B as
+// single bf16 values: dq and dk are off by 2.9e-3 of their norm, dbeta by 2.3e-3,
+// where rounding the exact values gives 1.7e-3.  Second parts would make a
+// slice's record 104 KB instead of 56, and a CTA holds two: more than an SM's
+// shared memory, for gradients that are bf16 when they leave.
 //
 // 4 x 2048 tokens, 16 heads of P 128 in 8 groups, N 128: pre-pass 52 us, states'
 // pass 119, gradients' chain 155 (both chains' latency: 64 CTAs, 32 blocks each),
@@ -623,6 +632,7 @@ struct GradArgs {
     int64_t nblk;
     int R, nsl;
 };
+// (cs in one part: a block that resets at every token reaches 1e4, where a step is 1e-3, half of bf16's)
 struct alignas(16) GradTab {
     float cs[kQ], beta[kQ], bg[kQ], w[kQ], gs[kQ];
     float total;

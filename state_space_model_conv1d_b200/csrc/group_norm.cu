@@ -8,8 +8,10 @@
 // contiguous stretch.  A unit stays with its group, which keeps the weights
 // (forward) and their gradients' sums (backward) in registers over its tokens.
 // Groups of 512, gate behind the norm: 402 MB in 75 us, 5.4 TB/s; groups of 64
-// with the gate in front, backward: 671 MB in 141 us, 4.8 TB/s.  Past 8192
-// channels a group the backward's registers spill.
+// with the gate in front, backward: 671 MB in 141 us, 4.8 TB/s.  Units of 512
+// threads have 128 registers a thread and spill: the backward from 4097 channels
+// a group on (up to 620 bytes a thread, past 8192 channels 1 to 2 KB), the
+// forward past 8192 with fp32 or a gate (60 to 390 bytes).
 //
 // Backward, with n the normalised values, t = n w + bias, dt = dL/dt, dn = dt w:
 //     ds = r (dn - n mean(dn n) - [subtract_mean] mean(dn)),  r = 1/sqrt(var + eps)

@@ -260,7 +260,8 @@ def _norm_args(x, groups, weight, bias, z, subtract_mean, eps, gate_first, activ
 
 def group_norm_fwd(x, groups, *, weight=None, bias=None, z=None, subtract_mean=False, eps=1e-5, gate_first=False,
                    activation=False, y=None, stream=None):
-    """Group norm of channels-last rows ``x [tokens, C]`` or ``[b, T, C]``, every token by itself.
+    """Group norm of channels-last rows ``x [tokens, C]`` or ``[b, T, C]``, every token by itself: statistics are
+    those of one token's group, not of the group over all positions as in ``torch.nn.GroupNorm``.
 
     ``n`` is x normalised per group (root mean square, or mean and variance
     with ``subtract_mean``), ``t = n * weight + bias`` (fp32 ``[C]``).  Returns
