@@ -63,6 +63,11 @@ static __device__ __noinline__ bool wait_slow(uint64_t *mb, volatile int *abort,
 SSM_DEVINL bool wait_bar(uint64_t *mb, volatile int *abort, uint32_t parity, int32_t *err) {
     return tc::mbar_try_wait(mb, parity) || wait_slow(mb, abort, parity, err);
 }
+// The same by a whole warp, whose lanes go on or give up together: what follows
+// are instructions that a warp issues as one.
+SSM_DEVINL bool wait_warp(uint64_t *mb, volatile int *abort, uint32_t parity, int32_t *err) {
+    return __all_sync(~0u, wait_bar(mb, abort, parity, err));
+}
 // Barrier 1 over `threads` threads that also tells whether `ok` holds in all of
 // them: warps that meet at a barrier give up together.
 template <int threads>

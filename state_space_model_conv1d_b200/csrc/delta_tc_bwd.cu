@@ -37,7 +37,7 @@
 // shared memory, for gradients that are bf16 when they leave.
 //
 // 4 x 2048 tokens, 16 heads of P 128 in 8 groups, N 128: pre-pass 52 us, states'
-// pass 119, gradients' chain 155 (both chains' latency: 64 CTAs, 32 blocks each),
+// pass 111, gradients' chain 150 (both chains' latency: 64 CTAs, 32 blocks each),
 // the blocks' gradients 124 (230 MB of kept operands; one CTA an SM, whose
 // products, passes and loads follow one another, 14k cycles a head).
 #include <string.h>
@@ -167,7 +167,7 @@ delta_bwd_chain_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, c
     const uint32_t tm = ax.tmem;
     volatile int *ab = &ax.abort;
     int32_t *err = p.sv.err;
-    auto wait = [&](int b, uint32_t parity) { return wait_bar(&ax.mb[b], ab, parity, err); };
+    auto wait = [&](int b, uint32_t parity) { return wait_warp(&ax.mb[b], ab, parity, err); };
     const uint32_t sb = tc::smem_u32(sm);
     // blocks run from the last: turn `it` is block n - 1 - it
     auto tokens = [&](int it) { return (int)min((int64_t)kQ, hi - lo - (int64_t)(n - 1 - it) * kQ); };

@@ -34,12 +34,13 @@
 // the other and make one operand of 128 rows, and so do the two T of a CTA
 // whose halves are different heads.
 //
-// 4 x 4096 tokens, 32 heads of P 128, N 128: 240 us, 64 blocks one after the
-// other in 128 CTAs, 3.7 us (6.8k cycles) a block: the chain's latency, 36 MMAs
+// 4 x 4096 tokens, 32 heads of P 128, N 128: 232 us, 64 blocks one after the
+// other in 128 CTAs, 3.6 us (6.6k cycles) a block: the chain's latency, 36 MMAs
 // of about 100 cycles and the passes between them.  28301 packed tokens, 64 heads
-// of P 64, two of them in a CTA: 450 us, 7.3k cycles a block.  (With the output's
+// of P 64, two of them in a CTA: 443 us, 7.2k cycles a block.  (With the output's
 // product in the MMA warp, whose waits then queue up behind the products already
-// issued, it was 257 and 472 us.)  The token-by-token form takes 15 times as long
+// issued, it was 17 and 22 us more; with waits whose outcome each lane keeps for
+// itself 8 and 7 us more.)  The token-by-token form takes 15 times as long
 // on the first call.
 #include <string.h>
 
@@ -177,7 +178,7 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
     const uint32_t tm = ax.tmem;
     volatile int *ab = &ax.abort;
     int32_t *err = p.sv.err;
-    auto wait = [&](int b, uint32_t parity) { return wait_bar(&ax.mb[b], ab, parity, err); };
+    auto wait = [&](int b, uint32_t parity) { return wait_warp(&ax.mb[b], ab, parity, err); };
     const uint32_t sb = tc::smem_u32(sm);
 
     if (warp < kChainWarps) {
