@@ -332,9 +332,14 @@ SSM_API ssm_status ssm_scan_fwd_noalloc(const ssm_scan_args *args, void *stream)
  * ssm_check_bounds_enabled: 1 in the checked build, 0 in libssm.so.
  * ssm_bounds_record: waits for the device, then reads the record into the
  * non-NULL pointers (code 0 when no check failed) and clears it when `clear`
- * is nonzero.  Returns SSM_ERR_UNSUPPORTED in the normal build. */
+ * is nonzero.  Returns SSM_ERR_UNSUPPORTED in the normal build.
+ * ssm_delta_wait_limit: how long a wait of the delta rule's tensor-core kernels
+ * lasts before the kernel gives up, sets SSM_DEVERR_TIMEOUT and leaves (2 s from
+ * the start; 0: at the first poll).  A test's way to make waits run out; waits
+ * for the device first.  Returns SSM_ERR_UNSUPPORTED in the normal build. */
 SSM_API int32_t ssm_check_bounds_enabled(void);
 SSM_API ssm_status ssm_bounds_record(int32_t *code, int32_t *site, int64_t *index, int64_t *extent, int32_t clear);
+SSM_API ssm_status ssm_delta_wait_limit(int64_t ns);
 
 /* Waits for `stream`, then reads the device error word of a workspace last
  * used by ssm_scan_fwd: SSM_OK, or SSM_ERR_DEVICE with *code set to an

@@ -209,6 +209,7 @@ SIGNATURES = {
     "ssm_pages_free": ([_args, _vp, C.c_size_t, _vp], _i32),
     "ssm_pages_compact": ([_args, _vp, C.c_size_t, _vp], _i32),
     "ssm_check_bounds_enabled": ([], _i32),
+    "ssm_delta_wait_limit": ([_i64], _i32),
     "ssm_bounds_record": ([C.POINTER(_i32), C.POINTER(_i32), C.POINTER(_i64), C.POINTER(_i64), _i32], _i32),
 }
 

@@ -92,6 +92,7 @@ struct BoundsRecord {
     long long index, extent;
 };
 extern __device__ BoundsRecord g_ssm_bounds;
+extern __device__ unsigned long long g_delta_wait_ns;    // ssm_delta_wait_limit()
 SSM_DEVINL bool bounds_ok(int64_t index, int64_t extent, int site) {
     if (index >= 0 && index < extent) return true;
     if (atomicCAS(&g_ssm_bounds.code, 0, SSM_DEVERR_BOUNDS) == 0) {

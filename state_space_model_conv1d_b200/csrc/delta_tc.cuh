@@ -45,6 +45,16 @@ SSM_DEVINL float bwd_beta(float b) { return fabsf(b) < kTinyBeta ? copysignf(kTi
 // pointer made from an integer would turn every access into a generic one.
 SSM_DEVINL uint8_t *smem_1024(uint8_t *raw) { return raw + ((0u - tc::smem_u32(raw)) & 1023u); }
 
+// How long a wait lasts before it gives up, and one look at the barrier.  In the
+// checked build the limit is a variable, so that a test can make waits run out
+// (ssm_delta_wait_limit), and a look does not sleep, so that short limits hold.
+#ifdef SSM_CHECK_BOUNDS
+SSM_DEVINL uint64_t wait_limit_ns() { return *(volatile unsigned long long *)&g_delta_wait_ns; }
+SSM_DEVINL bool poll(uint64_t *mb, uint32_t parity) { return tc::mbar_test_wait(mb, parity); }
+#else
+SSM_DEVINL uint64_t wait_limit_ns() { return 2000000000ull; }
+SSM_DEVINL bool poll(uint64_t *mb, uint32_t parity) { return tc::mbar_try_wait(mb, parity); }
+#endif
 // Wait for an mbarrier phase, at most two seconds; gives up as soon as another
 // thread of the CTA has (`abort`), and records the timeout in the error word.
 // The loop is kept out of line: a kernel of many roles waits in dozens of
@@ -53,15 +63,15 @@ static __device__ __noinline__ bool wait_slow(uint64_t *mb, volatile int *abort,
     const uint64_t t0 = tc::globaltimer_ns();
     for (;;) {
         if (*abort) return false;
-        if (tc::mbar_try_wait(mb, parity)) return true;
-        if (tc::globaltimer_ns() - t0 > 2000000000ull) break;
+        if (poll(mb, parity)) return true;
+        if (tc::globaltimer_ns() - t0 >= wait_limit_ns()) break;
     }
     *abort = 1;
     if (err) atomicExch(err, SSM_DEVERR_TIMEOUT);
     return false;
 }
 SSM_DEVINL bool wait_bar(uint64_t *mb, volatile int *abort, uint32_t parity, int32_t *err) {
-    return tc::mbar_try_wait(mb, parity) || wait_slow(mb, abort, parity, err);
+    return poll(mb, parity) || wait_slow(mb, abort, parity, err);
 }
 // The same by a whole warp, whose lanes go on or give up together: what follows
 // are instructions that a warp issues as one.

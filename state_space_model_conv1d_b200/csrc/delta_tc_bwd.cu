@@ -169,6 +169,7 @@ delta_bwd_chain_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, c
     int32_t *err = p.sv.err;
     auto wait = [&](int b, uint32_t parity) { return wait_warp(&ax.mb[b], ab, parity, err); };
     const uint32_t sb = tc::smem_u32(sm);
+    int issued = 0;                            // turns whose loads the load warp has issued
     // blocks run from the last: turn `it` is block n - 1 - it
     auto tokens = [&](int it) { return (int)min((int64_t)kQ, hi - lo - (int64_t)(n - 1 - it) * kQ); };
 
@@ -539,7 +540,6 @@ delta_bwd_chain_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, c
         }
     } else {
         // --------------------------------------------------- loads and gate tables
-        int issued = 0;
         for (int it = 0; it < n; ++it) {
             const int stg = it & 1, blk = n - 1 - it, nt = tokens(it);
             const int64_t t0 = lo + (int64_t)blk * kQ;
@@ -602,18 +602,24 @@ delta_bwd_chain_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, c
             __syncwarp();
             if (lane == 0) arrive(&ax.mb[B_TAB0 + stg]);
         }
-        if (*ab && lane == 0 && issued > 0) {      // copies in flight land before the CTA ends
-            for (int c = max(0, issued - 2); c < issued; ++c) tc::mbar_wait(&ax.mb[B_FULL0 + (c & 1)], (c >> 1) & 1, 1u << 22);
-            tc::mbar_wait(&ax.mb[B_PFULL], (issued - 1) & 1, 1u << 22);
-        }
-    }
-    if (*ab && lane == 0 && warp == kMmaWarp) {
-        tc::mma_commit(&ax.mb[B_DRAIN]);
-        tc::mbar_wait(&ax.mb[B_DRAIN], 0, 1u << 22);
     }
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
+    if (*ab) {                                 // (as in the forward chain)
+        if (warp < kMmaWarp) tmem_wait_st();
+        if (warp == kLoadWarp && lane == 0 && issued > 0) {
+            for (int c = max(0, issued - 2); c < issued; ++c) tc::mbar_wait(&ax.mb[B_FULL0 + (c & 1)], (c >> 1) & 1, 1u << 22);
+            tc::mbar_wait(&ax.mb[B_PFULL], (issued - 1) & 1, 1u << 22);
+        }
+        if (warp == kMmaWarp && lane == 0) {
+            tc::mma_commit(&ax.mb[B_DRAIN]);
+            tc::mbar_wait(&ax.mb[B_DRAIN], 0, 1u << 22);
+        }
+        __syncwarp();
+        tc::fence_before_sync();
+        __syncthreads();
+    }
     if (warp == 0) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tm, kTmemCols);
@@ -690,7 +696,7 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tm = ax.tmem, tl = tm + ((uint32_t)(32 * quarter) << 16);
-    uint32_t nfull = 0, ndone = 0;
+    uint32_t nfull = 0, ndone = 0, loads = 0, products = 0;    // phases waited for; (thread 0) started
     bool ok = true;
     auto full = [&] { ok = wait_bar(&ax.full, &ax.abort, nfull++ & 1, p.sv.err) && ok; };
     auto done = [&] {
@@ -700,11 +706,13 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
     // slices s0, s0 + 1 of a head's records
     auto load = [&](int head, int s0) {
         const int ns = min(2, p.nsl - s0);
+        ++loads;
         tc::mbar_expect_tx(&ax.full, ns * L::rec);
         for (int x = 0; x < ns; ++x)
             bulk_load(sm + L::REC + x * L::rec, p.rec.at(blockIdx.x, H, head, s0 + x), L::rec, &ax.full);
     };
     if (tid == 0) {
+        ++loads;
         tc::mbar_expect_tx(&ax.full, L::A);
 #pragma unroll
         for (int x = 0; x < NK / 64; ++x) {
@@ -731,6 +739,7 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
             tc::mma_bf16(tm + TG_K, dQK + o, dQK + (kTile >> 4) + o, tc::idesc_bf16(128, 64, 0, 0), kk > 0);
         }
         tc::mma_commit(&ax.done);
+        ++products;
     }
     __syncwarp();
     if (ok) done();
@@ -787,6 +796,7 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
                     }
                 }
                 tc::mma_commit(&ax.done);
+                ++products;
             }
             __syncwarp();
             for (int x = 0; x < ns; ++x) {
@@ -884,6 +894,7 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
                 tc::mma_bf16(tm + TG_A, dA + (((kk >> 2) * 2 * kTile + (kk & 3) * 32) >> 4), dQKm + kk * 128,
                              tc::idesc_bf16(128, NK, 0, 1), kk > 0);
             tc::mma_commit(&ax.done);
+            ++products;
         }
         __syncwarp();
         done();
@@ -979,11 +990,10 @@ delta_grad_kernel(const GradArgs p, const __grid_constant__ CUtensorMap tm_q, co
                     *reinterpret_cast<const uint4 *>(sm + L::A + (row * kRow + (c ^ (row & 7))) * 16);
         }
     }
-    if (!ok && tid == 0) {
-        // a wait ran out: what is in flight lands before the CTA ends
-        tc::mma_commit(&ax.done);
-        tc::mbar_wait(&ax.done, ndone & 1, 1u << 22);
-        tc::mbar_wait(&ax.full, nfull & 1, 1u << 22);
+    if (ax.abort && tid == 0) {
+        // a wait ran out: what is in flight (the last phase started of each barrier) lands before the CTA ends
+        if (products) tc::mbar_wait(&ax.done, (products - 1) & 1, 1u << 22);
+        if (loads) tc::mbar_wait(&ax.full, (loads - 1) & 1, 1u << 22);
     }
     __syncwarp();
     tc::fence_before_sync();

@@ -180,6 +180,7 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
     int32_t *err = p.sv.err;
     auto wait = [&](int b, uint32_t parity) { return wait_warp(&ax.mb[b], ab, parity, err); };
     const uint32_t sb = tc::smem_u32(sm);
+    int issued = 0;                            // blocks whose loads the load warp has issued
 
     if (warp < kChainWarps) {
         // ---------------------------------------------------------------- the chain
@@ -508,7 +509,6 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
         }
     } else {
         // --------------------------------------------------- loads and gate tables
-        int issued = 0;
         for (int c = 0; c < n; ++c) {
             const int stg = c & 1;
             const int64_t t0 = lo + (int64_t)c * kQ;
@@ -569,18 +569,25 @@ delta_fwd_kernel(const Args p, const __grid_constant__ CUtensorMap tm_q, const _
             __syncwarp();
             if (lane == 0) arrive(&ax.mb[B_TAB0 + stg]);
         }
-        if (*ab && lane == 0)                  // copies in flight land before the CTA ends
-            for (int c = max(0, issued - 2); c < issued; ++c) tc::mbar_wait(&ax.mb[B_FULL0 + (c & 1)], (c >> 1) & 1, 1u << 22);
-    }
-    if (*ab && lane == 0 && (warp == kMmaWarp || warp == kOut0)) {
-        // after a wait that ran out: the MMAs in flight complete before tensor memory is freed
-        const int b = warp == kMmaWarp ? B_DRAIN : B_DRAIN2;
-        tc::mma_commit(&ax.mb[b]);
-        tc::mbar_wait(&ax.mb[b], 0, 1u << 22);
     }
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
+    if (*ab) {
+        // A wait ran out, here or in a warp that came later than this one: what is in flight (copies, MMAs, stores to
+        // tensor memory) lands before tensor memory is freed and the CTA ends.
+        if (warp < kMmaWarp) tmem_wait_st();
+        if (warp == kLoadWarp && lane == 0)
+            for (int c = max(0, issued - 2); c < issued; ++c) tc::mbar_wait(&ax.mb[B_FULL0 + (c & 1)], (c >> 1) & 1, 1u << 22);
+        if (lane == 0 && (warp == kMmaWarp || warp == kOut0)) {
+            const int b = warp == kMmaWarp ? B_DRAIN : B_DRAIN2;
+            tc::mma_commit(&ax.mb[b]);
+            tc::mbar_wait(&ax.mb[b], 0, 1u << 22);
+        }
+        __syncwarp();
+        tc::fence_before_sync();
+        __syncthreads();
+    }
     if (warp == 0) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tm, kTmemCols);

@@ -12,6 +12,7 @@
 #ifdef SSM_CHECK_BOUNDS
 namespace ssm {
 __device__ BoundsRecord g_ssm_bounds;
+__device__ unsigned long long g_delta_wait_ns = 2000000000ull;
 }
 #endif
 
@@ -365,6 +366,17 @@ ssm_status ssm_bounds_record(int32_t *code, int32_t *site, int64_t *index, int64
     return SSM_OK;
 #else
     (void)code; (void)site; (void)index; (void)extent; (void)clear;
+    return SSM_ERR_UNSUPPORTED;
+#endif
+}
+
+ssm_status ssm_delta_wait_limit(int64_t ns) {
+    if (ns < 0) return SSM_ERR_INVALID_ARG;
+#ifdef SSM_CHECK_BOUNDS
+    SSM_TRY(cuda_status(cudaDeviceSynchronize()));
+    const unsigned long long v = (unsigned long long)ns;
+    return cuda_status(cudaMemcpyToSymbol(ssm::g_delta_wait_ns, &v, sizeof(v)));
+#else
     return SSM_ERR_UNSUPPORTED;
 #endif
 }
