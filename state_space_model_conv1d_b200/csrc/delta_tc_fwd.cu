@@ -18,10 +18,11 @@
 // 2^-17 each): h_final is off by 3.5e-6 of its norm after nine blocks, 1.2e-5
 // with keys alike and beta 2.  Of what only reaches y the attention weights are
 // rounded to bf16 once, like y itself: y is off by 2.1e-3 to 2.3e-3 of its norm,
-// and rounding the exact y gives 1.7e-3.  Their low part would need four more
-// products a block and head and 8 KB more a stage, for which a CTA of two heads
-// (218 of 227 KB) has no room.  u goes as two parts there too (with its high part
-// alone y was off by 2.6e-3, in 1.5 % less time).
+// and rounding the exact y gives 1.7e-3.  Their low part would make y's products
+// half as many again and its operand 16 KB instead of 8 a block and head, written
+// by a pre-pass that is bound by shared memory, for a y that is bf16 itself.  u
+// goes as two parts there too (with its high part alone y was off by 2.6e-3, in
+// 1.5 % less time).
 //
 // Roles: 8 warps for the chain (two per lane quarter, half of the columns
 // each), 4 for the output (one thread of them issues its product), one thread
