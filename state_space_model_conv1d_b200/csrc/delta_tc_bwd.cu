@@ -638,7 +638,8 @@ struct GradArgs {
     int64_t nblk;
     int R, nsl;
 };
-// (cs in one part: a block that resets at every token reaches 1e4, where a step is 1e-3, half of bf16's)
+// (cs in one part: after 64 resets it is 1e4, where its rounding moves a weight by 2^-11; the weight is then rounded
+// to bf16, up to 2^-8)
 struct alignas(16) GradTab {
     float cs[kQ], beta[kQ], bg[kQ], w[kQ], gs[kQ];
     float total;
